@@ -597,6 +597,190 @@ int zero_offload_step_amp(const zero_offload_tensor* tensors, int32_t T, int32_t
 int zero_offload_adamw_host(float* master, float* exp_avg, float* exp_avg_sq, const float* g, void* param_out,
                             int64_t n, const zero_adamw_hparams* hp, double clip_coef, int32_t threads);
 
+/* ------------------------------------------------------------------------
+ * Around a training block: 8-bit activation checkpoints and the gradients
+ * taken from them.
+ *
+ * "CS336 Lecture 7: Parallelism 1" counts activations (34 s*b*h bytes a layer,
+ * P2 section "激活内存") next to the 16 bytes per parameter that the calls above
+ * manage. These calls keep the rows that a block's backward pass needs in 8
+ * bits, and write the gradients of its matrices and norm vectors in the form
+ * that the calls above read: one bf16 gradient replica, or a sum added to an
+ * fp32 accumulator (micro-batch after micro-batch).
+ *
+ * A row-major operand is a zero_rows: any row stride ld >= the columns, any
+ * base that is a multiple of its element size (16-byte accesses are used at
+ * any alignment). Rows and columns beyond a call's sizes are neither read nor
+ * written. Vectors are zero_rows with one row, whose ld is ignored.
+ *
+ * The 8-bit form of rows x cols values (an "act8"): every row is cut into
+ * blocks of 32 columns (the last may be short); a block is stored as codes
+ * and one power of two 2^k, k the smallest integer >= -117 with
+ *   max |x| <= F * 2^k,   F = 448 (ZERO_ACT8_E4M3) or 127 (ZERO_ACT8_INT8),
+ * and code = x * 2^-k rounded to nearest even (e4m3 with its subnormals, or an
+ * integer). The scale is a power of two so that a decoded value, code * 2^k,
+ * has at most 7 significant bits and is exact in bf16: products of decoded
+ * values are products of what was saved. A block that holds an inf or NaN
+ * decodes to NaN in every element, so that it reaches the gradients and their
+ * found_inf. (A finite value that rounds up to 2^128 decodes to infinity.)
+ * In memory, P = cols rounded up to 32: rows * P code bytes, row by row, the
+ * columns from cols on 0, then rows * P/32 scale bytes k + 127 (255: NaN).
+ * The buffer is 16-byte aligned, zero_act8_bytes(rows, cols) bytes.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of a zero_rows. */
+#define ZERO_BF16 1
+#define ZERO_F32 2
+
+/* 8-bit code formats. e4m3 keeps small values beside large ones (half a step
+ * is 2^-4 of the value); int8 has an even step (half of it is at most 1/127 of
+ * the block's largest value, and no less than 1/254). */
+#define ZERO_ACT8_E4M3 1
+#define ZERO_ACT8_INT8 2
+
+/* flag of zero_act8_wgrad and zero_block_norm_grad: add to the gradient
+ * buffers, which are then fp32; otherwise they are overwritten */
+#define ZERO_GRAD_ACCUMULATE 1
+
+/* Largest cols of zero_block_norm and zero_block_norm_grad, whose rows stay
+ * in the registers of one workgroup. */
+#define ZERO_BLOCK_NORM_MAX_COLS 16384
+
+/* A row-major matrix in device memory (the struct itself is host memory). */
+typedef struct zero_rows {
+    void* data;       /* device; NULL: the operand is absent */
+    int64_t ld;       /* elements from one row to the next, >= the columns */
+    int32_t dtype;    /* ZERO_BF16 or ZERO_F32 */
+    int32_t reserved; /* must be 0 */
+} zero_rows;
+
+/* zero_act8_bytes -- size of an act8 buffer; 0 on invalid sizes. */
+size_t zero_act8_bytes(int64_t rows, int64_t cols);
+
+/*
+ * zero_act8_save -- x (rows x cols, bf16 or fp32) into the act8 buffer ckpt.
+ * zero_act8_load -- the act8 buffer ckpt into out (rows x cols, bf16 or fp32),
+ * exactly. 0 <= rows < 2^31, 0 <= cols <= 2^30, rows * P < 2^36; rows or cols 0
+ * is a no-op.
+ */
+int zero_act8_save(const zero_rows* x, int64_t rows, int64_t cols, int32_t format, void* ckpt, hipStream_t stream);
+int zero_act8_load(const void* ckpt, int64_t rows, int64_t cols, int32_t format, const zero_rows* out,
+                   hipStream_t stream);
+
+/*
+ * zero_act8_wgrad_workspace_bytes -- workspace size of zero_act8_wgrad (the
+ * partial sums of a product that is split over its rows; often 0); also 0 on
+ * invalid sizes.
+ */
+size_t zero_act8_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols);
+
+/*
+ * zero_act8_wgrad -- the weight gradient of a linear layer out = in * W^T from
+ * the gradient dy of its output (rows x outs, bf16) and its input saved in 8
+ * bits (rows x cols):
+ *   dw[o][i] (+)= col_scale[i] * sum_t dy[t][o] * x[t][i]
+ * summed in fp32 in an order that depends only on the sizes. col_scale (cols
+ * values, bf16 or fp32; NULL: ones) is the weight of the norm before the
+ * layer when the checkpoint holds that norm's rows before their weight, as
+ * zero_block_norm saves them. dw (outs x cols): bf16 (a gradient replica) or
+ * fp32; with ZERO_GRAD_ACCUMULATE in flags, fp32 and added to. rows == 0
+ * writes zeros (nothing with ZERO_GRAD_ACCUMULATE). rows, outs < 2^31, cols <=
+ * 2^30, and dw has fewer than 2^22 tiles of 128 x 128 (6.8e10 elements).
+ * ws: device workspace of zero_act8_wgrad_workspace_bytes(...) bytes, 16-byte
+ * aligned (NULL if that is 0), contents irrelevant on entry and not kept; two
+ * calls that share one must not run concurrently.
+ */
+int zero_act8_wgrad(const zero_rows* dy, const void* ckpt, int64_t rows, int64_t outs, int64_t cols, int32_t format,
+                    const zero_rows* col_scale, const zero_rows* dw, int32_t flags, void* ws, size_t ws_bytes,
+                    hipStream_t stream);
+
+/*
+ * The boundary between two blocks: the norm after a block, its gate, the
+ * residual scale, the residual add, and the norm before the next block, in
+ * one pass. With n(z) = z / sqrt(mean(z^2) + eps) over a row, per row t:
+ *   yn    = n(y) when w_post is given, else y
+ *   x_out = x + residual_scale * gate[t / gate_rows] * (w_post * yn)
+ *   xn    = n(x_out)                       of x_out as stored, in its type
+ *   h     = w_pre * xn
+ * Absent operands (data NULL): y (then x_out is x itself and is not written),
+ * w_post (no norm after the block), gate (ones), w_pre (no norm before the
+ * next block). rstd_post and rstd_pre (fp32, one per row) are the reciprocal
+ * roots; ckpt_post and ckpt_pre the act8 buffers of yn and xn. All sums are
+ * fp32; every output is rounded once.
+ */
+typedef struct zero_block_norm_args {
+    int64_t rows;          /* 0 <= rows < 2^31 */
+    int64_t cols;          /* 0 <= cols <= ZERO_BLOCK_NORM_MAX_COLS */
+    int64_t gate_rows;     /* rows in a row that share one row of gate, >= 1 with a gate */
+    double residual_scale; /* finite; rounded to fp32 */
+    double eps;            /* finite, >= 0; rounded to fp32 */
+    zero_rows x;           /* residual stream, bf16 or fp32 */
+    zero_rows y;           /* block output, bf16 */
+    zero_rows w_post;      /* cols, bf16 or fp32 */
+    zero_rows gate;        /* ceil(rows / gate_rows) x cols, bf16 or fp32; needs y */
+    zero_rows w_pre;       /* cols, bf16 or fp32 */
+    zero_rows x_out;       /* residual stream, the type of x; written with y, may be x itself */
+    zero_rows h;           /* bf16, written with w_pre */
+    float* rstd_post;      /* rows, or NULL */
+    float* rstd_pre;       /* rows, or NULL */
+    void* ckpt_post;       /* act8 buffer, or NULL */
+    void* ckpt_pre;        /* act8 buffer, or NULL; needs w_pre */
+    int32_t format;        /* of both act8 buffers */
+    int32_t reserved;      /* must be 0 */
+} zero_block_norm_args;
+
+int zero_block_norm(const zero_block_norm_args* args, hipStream_t stream);
+
+/*
+ * zero_block_norm_grad -- the gradients of zero_block_norm. yn and xn come
+ * from act8 buffers, or (ckpt_* NULL) from y * rstd_post and x_out *
+ * rstd_pre. With g = residual_scale * gate, per row:
+ *   d    = dx_out + rstd_pre * (w_pre * dh - xn * mean(w_pre * dh * xn))
+ *   dx   = d                       (the gradient of x)
+ *   dy   = rstd_post * (w_post * g * d - yn * mean(w_post * g * d * yn)),
+ *          or g * d without w_post
+ * and, summed over rows in fp32 in an order that depends only on the sizes:
+ *   dw_pre = sum dh * xn,   dw_post = sum g * d * yn,
+ *   dgate[j] = sum over the rows of gate row j of residual_scale * d * w_post * yn.
+ * Absent (data NULL): dh (no norm before the next block; then dx_out is
+ * given), dx_out (zeros), dy and what only it needs (no block output: dx
+ * alone), and each of dw_pre, dw_post and dgate that is not wanted. dx may be
+ * dx_out itself. rows == 0 writes zeros to dw_pre and dw_post.
+ */
+typedef struct zero_block_norm_grad_args {
+    int64_t rows;
+    int64_t cols;
+    int64_t gate_rows;
+    double residual_scale;
+    zero_rows dh;     /* gradient of h, bf16 */
+    zero_rows dx_out; /* gradient of x_out from what follows, the type of dx */
+    zero_rows w_post; /* as in zero_block_norm */
+    zero_rows gate;
+    zero_rows w_pre;           /* with dh */
+    zero_rows x_out;           /* when dh is given and ckpt_pre is NULL: the type of dx */
+    zero_rows y;               /* when yn is needed and ckpt_post is NULL: bf16 */
+    const void* ckpt_pre;      /* act8 buffer of xn, or NULL */
+    const void* ckpt_post;     /* act8 buffer of yn, or NULL */
+    const float* rstd_pre;     /* rows, with dh */
+    const float* rstd_post;    /* rows, with w_post */
+    zero_rows dx;              /* the gradient of x, bf16 or fp32 */
+    zero_rows dy;              /* bf16 */
+    zero_rows dw_pre;          /* cols, bf16 or fp32 */
+    zero_rows dw_post;         /* cols, bf16 or fp32; needs w_post */
+    zero_rows dgate;           /* ceil(rows / gate_rows) x cols, bf16 or fp32; needs gate */
+    int32_t format;            /* of the act8 buffers */
+    int32_t flags;             /* ZERO_GRAD_ACCUMULATE: dw_pre, dw_post and dgate are fp32 and added to */
+} zero_block_norm_grad_args;
+
+/* Workspace size of zero_block_norm_grad (partial column sums); gate_rows 0
+ * without a gate; 0 on invalid sizes. */
+size_t zero_block_norm_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows);
+
+/* ws: device workspace of that size, 16-byte aligned (NULL if it is 0),
+ * contents irrelevant on entry and not kept; two calls that share one must not
+ * run concurrently. */
+int zero_block_norm_grad(const zero_block_norm_grad_args* args, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /*
  * zero_workspace_forget -- drop the host-side record that `ws` holds the
  * tensor table of an earlier zero_step, zero_step_amp, zero_bucket_reduce,

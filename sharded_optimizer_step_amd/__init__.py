@@ -34,6 +34,13 @@ Functions keep the C names:
   ``zero_offload_adamw_host(master, exp_avg, exp_avg_sq, g, param_out, hp, clip_coef, threads)``
 * ``zero_bucket_reduce_amp``, ``zero_step_accumulated_amp``, ``zero_offload_step_amp``: the same under the
   dynamic loss scale
+* ``zero_act8_save(x, ckpt)``, ``zero_act8_load(ckpt, out)``: activation rows to and from an 8-bit checkpoint
+  (``Act8``, made by ``new_act8(rows, cols, format)``)
+* ``zero_act8_wgrad_workspace_bytes(rows, outs, cols)``, ``zero_act8_wgrad(dy, ckpt, dw, flags, ws, col_scale=None)``:
+  a linear layer's weight gradient from its 8-bit input, as a bf16 replica or into an fp32 accumulator
+* ``zero_block_norm(BlockNorm(...))``, ``zero_block_norm_grad_workspace_bytes(rows, cols, gate_rows)``,
+  ``zero_block_norm_grad(BlockNormGrad(...), flags, ws)``: the norms after a block and before the next one, fused
+  with the block's gate, the residual scale and the residual add, forward and backward
 * ``zero_workspace_forget(ws)``, ``zero_status_string(status)``
 """
 from __future__ import annotations
@@ -65,6 +72,10 @@ BUCKET_STREAM_STORES = 4
 # steps above this many parameters write more than the 256 MiB Infinity Cache holds
 STREAM_STORES_MIN_PARAMS = (256 << 20) // 14
 BUCKET_PARTIAL_BYTES = 32
+ACT8_E4M3 = 1
+ACT8_INT8 = 2
+GRAD_ACCUMULATE = 1
+BLOCK_NORM_MAX_COLS = 16384
 
 # Every symbol the C ABI exports (include/zero_step.h).
 EXPORTS = ("zero_shard_reduce", "zero_grad_check_norm_workspace_bytes", "zero_grad_check_norm", "zero_adamw_step",
@@ -74,7 +85,9 @@ EXPORTS = ("zero_shard_reduce", "zero_grad_check_norm_workspace_bytes", "zero_gr
            "zero_offload_workspace_bytes", "zero_offload_host_workspace_bytes", "zero_offload_step",
            "zero_offload_adamw_host", "zero_bucket_reduce_amp", "zero_step_accumulated_amp",
            "zero_offload_step_amp", "zero_workspace_forget", "zero_status_string", "zero_step_noalloc",
-           "zero_bucket_step_workspace_bytes", "zero_bucket_step")
+           "zero_bucket_step_workspace_bytes", "zero_bucket_step", "zero_act8_bytes", "zero_act8_save",
+           "zero_act8_load", "zero_act8_wgrad_workspace_bytes", "zero_act8_wgrad", "zero_block_norm",
+           "zero_block_norm_grad_workspace_bytes", "zero_block_norm_grad")
 LOSS_SCALE_BYTES = 16
 
 
@@ -118,6 +131,28 @@ class _CResult(ctypes.Structure):
 class _CLossScaleConfig(ctypes.Structure):
     _fields_ = [("initial_scale_power", ctypes.c_int32), ("window", ctypes.c_int32), ("hysteresis", ctypes.c_int32),
                 ("min_scale", ctypes.c_float)]
+
+
+class _CRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class _CBlockNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+                ("residual_scale", ctypes.c_double), ("eps", ctypes.c_double), ("x", _CRows), ("y", _CRows),
+                ("w_post", _CRows), ("gate", _CRows), ("w_pre", _CRows), ("x_out", _CRows), ("h", _CRows),
+                ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p), ("ckpt_post", ctypes.c_void_p),
+                ("ckpt_pre", ctypes.c_void_p), ("format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _CBlockNormGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+                ("residual_scale", ctypes.c_double), ("dh", _CRows), ("dx_out", _CRows), ("w_post", _CRows),
+                ("gate", _CRows), ("w_pre", _CRows), ("x_out", _CRows), ("y", _CRows), ("ckpt_pre", ctypes.c_void_p),
+                ("ckpt_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p), ("rstd_post", ctypes.c_void_p),
+                ("dx", _CRows), ("dy", _CRows), ("dw_pre", _CRows), ("dw_post", _CRows), ("dgate", _CRows),
+                ("format", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
 class ZeroError(RuntimeError):
@@ -194,6 +229,23 @@ def lib() -> ctypes.CDLL:
         L.zero_offload_step_amp.argtypes = [ctypes.POINTER(_COffloadTensor), i32, i32, ctypes.POINTER(_CHparams), lsc,
                                             vp, dbl, vp, sz, vp, sz, ctypes.POINTER(_CResult), i32, vp]
         L.zero_offload_step_amp.restype = ctypes.c_int
+        rows = ctypes.POINTER(_CRows)
+        L.zero_act8_bytes.argtypes = [i64, i64]
+        L.zero_act8_bytes.restype = sz
+        L.zero_act8_save.argtypes = [rows, i64, i64, i32, vp, vp]
+        L.zero_act8_save.restype = ctypes.c_int
+        L.zero_act8_load.argtypes = [vp, i64, i64, i32, rows, vp]
+        L.zero_act8_load.restype = ctypes.c_int
+        L.zero_act8_wgrad_workspace_bytes.argtypes = [i64, i64, i64]
+        L.zero_act8_wgrad_workspace_bytes.restype = sz
+        L.zero_act8_wgrad.argtypes = [rows, vp, i64, i64, i64, i32, rows, rows, i32, vp, sz, vp]
+        L.zero_act8_wgrad.restype = ctypes.c_int
+        L.zero_block_norm.argtypes = [ctypes.POINTER(_CBlockNorm), vp]
+        L.zero_block_norm.restype = ctypes.c_int
+        L.zero_block_norm_grad_workspace_bytes.argtypes = [i64, i64, i64]
+        L.zero_block_norm_grad_workspace_bytes.restype = sz
+        L.zero_block_norm_grad.argtypes = [ctypes.POINTER(_CBlockNormGrad), vp, sz, vp]
+        L.zero_block_norm_grad.restype = ctypes.c_int
         L.zero_workspace_forget.argtypes = [vp]
         L.zero_workspace_forget.restype = ctypes.c_int
         L.zero_status_string.argtypes = [ctypes.c_int]
@@ -833,6 +885,235 @@ def zero_offload_step_amp(tensors: Sequence[OffloadTensor], hp: HParams, cfg: "L
            "zero_offload_step_amp")
     return dict(sumsq=r.sumsq, grad_norm=r.grad_norm, clip_coef=r.clip_coef, found_inf=r.found_inf,
                 skipped=r.skipped, status=r.status)
+
+
+# ---------------------------------------------------------------- around a training block
+
+_DTYPES = {torch.bfloat16: 1, torch.float32: 2}  # ZERO_BF16, ZERO_F32
+
+
+@dataclasses.dataclass
+class Act8:
+    """Rows of activations in 8 bits: rows x cols codes (ACT8_E4M3 or
+    ACT8_INT8) with a power-of-two scale for each 32 columns, in one device
+    buffer of zero_act8_bytes(rows, cols) bytes whose layout
+    include/zero_step.h gives."""
+    rows: int
+    cols: int
+    format: int
+    buf: torch.Tensor
+
+
+def zero_act8_bytes(rows: int, cols: int) -> int:
+    return int(lib().zero_act8_bytes(int(rows), int(cols)))
+
+
+def new_act8(rows: int, cols: int, format: int = ACT8_E4M3, device=None) -> Act8:
+    """An empty checkpoint of rows x cols."""
+    n = zero_act8_bytes(rows, cols)
+    if n == 0 and rows != 0 and cols != 0:
+        raise ValueError(f"no checkpoint of {rows} x {cols}")
+    return Act8(rows, cols, format, torch.empty(n, dtype=torch.uint8, device=device or "cuda"))
+
+
+class _Marshal:
+    """Checks the operands of one call: device tensors on the current device,
+    with the shapes and types that the call takes, as the C structures."""
+
+    def __init__(self):
+        self.device = torch.cuda.current_device()
+
+    def _on(self, t, name):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be a device tensor")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name}: on device {t.get_device()}, the current device is {self.device}")
+
+    def rows(self, t, name: str, shape, dtypes=(torch.bfloat16, torch.float32)) -> _CRows:
+        """A row-major matrix of any row stride; a vector is one row. None: absent."""
+        if t is None:
+            return _CRows()
+        self._on(t, name)
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.dim() == 1:
+            t = t.unsqueeze(0)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: the elements of a row must lie next to each other")
+        ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+        if ld < t.shape[1]:
+            raise ValueError(f"{name}: rows overlap")
+        return _CRows(t.data_ptr(), ld, _DTYPES[t.dtype], 0)
+
+    def f32(self, t, name: str, n: int):
+        if t is None:
+            return None
+        self._on(t, name)
+        _need(t, torch.float32, name, n)
+        return t.data_ptr()
+
+    def act8(self, c, name: str, rows: int, cols: int):
+        if c is None:
+            return None
+        if not isinstance(c, Act8):
+            raise TypeError(f"{name}: expected an Act8")
+        if (c.rows, c.cols) != (rows, cols):
+            raise ValueError(f"{name}: holds {c.rows} x {c.cols}, expected {rows} x {cols}")
+        self._on(c.buf, name)
+        _need(c.buf, torch.uint8, name)
+        if c.buf.numel() < zero_act8_bytes(rows, cols):
+            raise ValueError(f"{name}: {c.buf.numel()} bytes for {rows} x {cols}")
+        return c.buf.data_ptr()
+
+    def ws(self, ws):
+        if ws is not None:
+            _need_ws(ws)
+            self._on(ws, "ws")
+        return _ptr(ws), _need_ws(ws)
+
+
+def _matrix_shape(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
+    return int(t.shape[0]), int(t.shape[1])
+
+
+def zero_act8_save(x: torch.Tensor, ckpt: Act8, stream=None) -> None:
+    m = _Marshal()
+    rows, cols = _matrix_shape(x, "x")
+    r = m.rows(x, "x", (rows, cols))
+    _check(lib().zero_act8_save(ctypes.byref(r), rows, cols, int(ckpt.format), m.act8(ckpt, "ckpt", rows, cols),
+                                _stream(stream)), "zero_act8_save")
+
+
+def zero_act8_load(ckpt: Act8, out: torch.Tensor, stream=None) -> None:
+    m = _Marshal()
+    rows, cols = _matrix_shape(out, "out")
+    r = m.rows(out, "out", (rows, cols))
+    _check(lib().zero_act8_load(m.act8(ckpt, "ckpt", rows, cols), rows, cols, int(ckpt.format), ctypes.byref(r),
+                                _stream(stream)), "zero_act8_load")
+
+
+def zero_act8_wgrad_workspace_bytes(rows: int, outs: int, cols: int) -> int:
+    return int(lib().zero_act8_wgrad_workspace_bytes(int(rows), int(outs), int(cols)))
+
+
+def zero_act8_wgrad(dy: torch.Tensor, ckpt: Act8, dw: torch.Tensor, flags: int = 0, ws: Optional[torch.Tensor] = None,
+                    col_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dw (outs x cols, bf16 or fp32) = dy^T times the checkpoint's rows, its
+    columns times col_scale; with GRAD_ACCUMULATE added to an fp32 dw."""
+    m = _Marshal()
+    rows, outs = _matrix_shape(dy, "dy")
+    cols = int(ckpt.cols)
+    cdy = m.rows(dy, "dy", (rows, outs), (torch.bfloat16,))
+    cdw = m.rows(dw, "dw", (outs, cols))
+    scale = m.rows(col_scale, "col_scale", (1, cols))
+    wsp, wsb = m.ws(ws)
+    _check(lib().zero_act8_wgrad(ctypes.byref(cdy), m.act8(ckpt, "ckpt", rows, cols), rows, outs, cols,
+                                 int(ckpt.format), ctypes.byref(scale) if col_scale is not None else None,
+                                 ctypes.byref(cdw), int(flags), wsp, wsb, _stream(stream)), "zero_act8_wgrad")
+
+
+@dataclasses.dataclass
+class BlockNorm:
+    """The operands of zero_block_norm; None is an absent one. x and x_out:
+    the residual stream (bf16 or fp32); y and h: bf16; w_post, gate and w_pre:
+    bf16 or fp32; rstd_*: fp32; ckpt_*: Act8 of one format. gate has a row for
+    every gate_rows rows."""
+    x: torch.Tensor
+    y: Optional[torch.Tensor] = None
+    w_post: Optional[torch.Tensor] = None
+    gate: Optional[torch.Tensor] = None
+    w_pre: Optional[torch.Tensor] = None
+    x_out: Optional[torch.Tensor] = None
+    h: Optional[torch.Tensor] = None
+    rstd_post: Optional[torch.Tensor] = None
+    rstd_pre: Optional[torch.Tensor] = None
+    ckpt_post: Optional[Act8] = None
+    ckpt_pre: Optional[Act8] = None
+    gate_rows: int = 0
+    residual_scale: float = 1.0
+    eps: float = 1e-6
+
+
+@dataclasses.dataclass
+class BlockNormGrad:
+    """The operands of zero_block_norm_grad; None is an absent one. Saved rows
+    come from ckpt_* or, without one, from x_out and y."""
+    dx: torch.Tensor
+    dx_out: Optional[torch.Tensor] = None
+    dh: Optional[torch.Tensor] = None
+    w_post: Optional[torch.Tensor] = None
+    gate: Optional[torch.Tensor] = None
+    w_pre: Optional[torch.Tensor] = None
+    x_out: Optional[torch.Tensor] = None
+    y: Optional[torch.Tensor] = None
+    ckpt_pre: Optional[Act8] = None
+    ckpt_post: Optional[Act8] = None
+    rstd_pre: Optional[torch.Tensor] = None
+    rstd_post: Optional[torch.Tensor] = None
+    dy: Optional[torch.Tensor] = None
+    dw_pre: Optional[torch.Tensor] = None
+    dw_post: Optional[torch.Tensor] = None
+    dgate: Optional[torch.Tensor] = None
+    gate_rows: int = 0
+    residual_scale: float = 1.0
+
+
+def _act8_format(*ckpts) -> int:
+    formats = {int(c.format) for c in ckpts if c is not None}
+    if len(formats) > 1:
+        raise ValueError("ckpt_post and ckpt_pre have different formats")
+    return formats.pop() if formats else 0
+
+
+def _gates(rows: int, gate_rows: int) -> int:
+    if gate_rows < 1:
+        raise ValueError(f"gate_rows: {gate_rows} with a gate")
+    return -(-rows // gate_rows)
+
+
+def zero_block_norm(b: BlockNorm, stream=None) -> None:
+    m = _Marshal()
+    rows, cols = _matrix_shape(b.x, "x")
+    full, one, bf16 = (rows, cols), (1, cols), (torch.bfloat16,)
+    c = _CBlockNorm(rows, cols, int(b.gate_rows), float(b.residual_scale), float(b.eps), m.rows(b.x, "x", full),
+                    m.rows(b.y, "y", full, bf16), m.rows(b.w_post, "w_post", one),
+                    m.rows(b.gate, "gate", (_gates(rows, b.gate_rows), cols)) if b.gate is not None else _CRows(),
+                    m.rows(b.w_pre, "w_pre", one), m.rows(b.x_out, "x_out", full, (b.x.dtype,)),
+                    m.rows(b.h, "h", full, bf16), m.f32(b.rstd_post, "rstd_post", rows),
+                    m.f32(b.rstd_pre, "rstd_pre", rows), m.act8(b.ckpt_post, "ckpt_post", rows, cols),
+                    m.act8(b.ckpt_pre, "ckpt_pre", rows, cols), _act8_format(b.ckpt_post, b.ckpt_pre), 0)
+    _check(lib().zero_block_norm(ctypes.byref(c), _stream(stream)), "zero_block_norm")
+
+
+def zero_block_norm_grad_workspace_bytes(rows: int, cols: int, gate_rows: int) -> int:
+    """gate_rows: 0 without a gate."""
+    return int(lib().zero_block_norm_grad_workspace_bytes(int(rows), int(cols), int(gate_rows)))
+
+
+def zero_block_norm_grad(b: BlockNormGrad, flags: int = 0, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    m = _Marshal()
+    rows, cols = _matrix_shape(b.dx, "dx")
+    full, one, bf16, like = (rows, cols), (1, cols), (torch.bfloat16,), (b.dx.dtype,)
+    gates = (_gates(rows, b.gate_rows), cols) if b.gate is not None else (0, cols)
+    c = _CBlockNormGrad(rows, cols, int(b.gate_rows), float(b.residual_scale), m.rows(b.dh, "dh", full, bf16),
+                        m.rows(b.dx_out, "dx_out", full, like), m.rows(b.w_post, "w_post", one),
+                        m.rows(b.gate, "gate", gates), m.rows(b.w_pre, "w_pre", one),
+                        m.rows(b.x_out, "x_out", full, like), m.rows(b.y, "y", full, bf16),
+                        m.act8(b.ckpt_pre, "ckpt_pre", rows, cols), m.act8(b.ckpt_post, "ckpt_post", rows, cols),
+                        m.f32(b.rstd_pre, "rstd_pre", rows), m.f32(b.rstd_post, "rstd_post", rows),
+                        m.rows(b.dx, "dx", full), m.rows(b.dy, "dy", full, bf16), m.rows(b.dw_pre, "dw_pre", one),
+                        m.rows(b.dw_post, "dw_post", one), m.rows(b.dgate, "dgate", gates),
+                        _act8_format(b.ckpt_post, b.ckpt_pre), int(flags))
+    wsp, wsb = m.ws(ws)
+    _check(lib().zero_block_norm_grad(ctypes.byref(c), wsp, wsb, _stream(stream)), "zero_block_norm_grad")
 
 
 def zero_workspace_forget(ws: torch.Tensor) -> None:

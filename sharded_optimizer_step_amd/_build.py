@@ -3,13 +3,16 @@ kernels and the C ABI with hipcc (it cross-compiles without a GPU), the host
 optimizer of the CPU-offloaded step with g++."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, "zero_kernels.hip"), os.path.join(CSRC, "zero_api.cpp")]
+# compiled side by side: each has its own kernels (no device code is shared between objects)
+SOURCES = [os.path.join(CSRC, f) for f in ("zero_kernels.hip", "zero_api.cpp", "zero_act8.hip", "zero_wgrad.hip",
+                                            "zero_block_norm.hip", "zero_block_api.cpp")]
 # host-only C++ (the optimizer half of the CPU-offloaded step), built by the
 # host compiler into an object that the library links
 HOST_SOURCES = [os.path.join(CSRC, "zero_host_adamw.cpp")]
@@ -35,23 +38,26 @@ HIPCC_FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(OBJ_DIR, exist_ok=True)
-    objs = []
-    for src in HOST_SOURCES:
-        obj = os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
-        cmd = ["g++", *HOST_FLAGS, "-I", CSRC, "-c", "-o", obj, src]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("g++ failed:\n" + r.stdout + r.stderr)
-        objs.append(obj)
-    tmp = LIB + ".tmp"
-    cmd = ["hipcc", *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp, *SOURCES, "-x", "none", *objs,
-           "-lpthread"]
+def _run(cmd) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     out = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in l)
     if r.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + out)
+        raise RuntimeError(f"{cmd[0]} failed:\n" + out)
+    return out
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    obj = lambda src: os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
+    compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    cmds = [["g++", *HOST_FLAGS, "-I", CSRC, "-c", "-o", obj(s), s] for s in HOST_SOURCES]
+    cmds += [["hipcc", *compile_flags, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c", "-o", obj(s), s]
+             for s in SOURCES]
+    with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+        out = "\n".join(o for o in pool.map(_run, cmds) if o.strip())
+    tmp = LIB + ".tmp"
+    link = [f for f in HIPCC_FLAGS if f in ("-fPIC", "-shared") or f.startswith("--offload-arch")]
+    out += _run(["hipcc", *link, "-o", tmp, *[obj(s) for s in SOURCES + HOST_SOURCES], "-lpthread"])
     if verbose and out.strip():
         print(out)
     os.replace(tmp, LIB)
