@@ -229,7 +229,7 @@ def lib() -> ctypes.CDLL:
         L.zero_offload_step_amp.argtypes = [ctypes.POINTER(_COffloadTensor), i32, i32, ctypes.POINTER(_CHparams), lsc,
                                             vp, dbl, vp, sz, vp, sz, ctypes.POINTER(_CResult), i32, vp]
         L.zero_offload_step_amp.restype = ctypes.c_int
-        rows = ctypes.POINTER(_CRows)
+        rows = vp  # a zero_rows, as packed bytes or by reference
         L.zero_act8_bytes.argtypes = [i64, i64]
         L.zero_act8_bytes.restype = sz
         L.zero_act8_save.argtypes = [rows, i64, i64, i32, vp, vp]
@@ -240,11 +240,11 @@ def lib() -> ctypes.CDLL:
         L.zero_act8_wgrad_workspace_bytes.restype = sz
         L.zero_act8_wgrad.argtypes = [rows, vp, i64, i64, i64, i32, rows, rows, i32, vp, sz, vp]
         L.zero_act8_wgrad.restype = ctypes.c_int
-        L.zero_block_norm.argtypes = [ctypes.POINTER(_CBlockNorm), vp]
+        L.zero_block_norm.argtypes = [vp, vp]
         L.zero_block_norm.restype = ctypes.c_int
         L.zero_block_norm_grad_workspace_bytes.argtypes = [i64, i64, i64]
         L.zero_block_norm_grad_workspace_bytes.restype = sz
-        L.zero_block_norm_grad.argtypes = [ctypes.POINTER(_CBlockNormGrad), vp, sz, vp]
+        L.zero_block_norm_grad.argtypes = [vp, vp, sz, vp]
         L.zero_block_norm_grad.restype = ctypes.c_int
         L.zero_workspace_forget.argtypes = [vp]
         L.zero_workspace_forget.restype = ctypes.c_int
@@ -916,64 +916,93 @@ def new_act8(rows: int, cols: int, format: int = ACT8_E4M3, device=None) -> Act8
     return Act8(rows, cols, format, torch.empty(n, dtype=torch.uint8, device=device or "cuda"))
 
 
-class _Marshal:
-    """Checks the operands of one call: device tensors on the current device,
-    with the shapes and types that the call takes, as the C structures."""
+# Marshalling of these calls: their operands are many and some of their
+# launches short, so it reads each tensor's attributes once and packs the C
+# structures in one step (a zero_rows is data, ld, dtype, reserved).
+_ROWS = struct.Struct("=QqiI")
+_BLOCK_NORM = struct.Struct("=qqqdd" + "QqiI" * 7 + "QQQQii")
+_BLOCK_NORM_GRAD = struct.Struct("=qqqd" + "QqiI" * 7 + "QQQQ" + "QqiI" * 5 + "ii")
+_ABSENT = (0, 0, 0, 0)
 
-    def __init__(self):
-        self.device = torch.cuda.current_device()
 
-    def _on(self, t, name):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name}: must be a device tensor")
-        if t.get_device() != self.device:
-            raise ValueError(f"{name}: on device {t.get_device()}, the current device is {self.device}")
+def _device_of(t, name: str) -> int:
+    """The current device, which a call's first operand has to be on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
+    return dev
 
-    def rows(self, t, name: str, shape, dtypes=(torch.bfloat16, torch.float32)) -> _CRows:
-        """A row-major matrix of any row stride; a vector is one row. None: absent."""
-        if t is None:
-            return _CRows()
-        self._on(t, name)
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-        if t.dim() == 1:
-            t = t.unsqueeze(0)
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}: the elements of a row must lie next to each other")
-        ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-        if ld < t.shape[1]:
-            raise ValueError(f"{name}: rows overlap")
-        return _CRows(t.data_ptr(), ld, _DTYPES[t.dtype], 0)
 
-    def f32(self, t, name: str, n: int):
-        if t is None:
-            return None
-        self._on(t, name)
-        _need(t, torch.float32, name, n)
-        return t.data_ptr()
+def _on(t, name: str, dev: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
 
-    def act8(self, c, name: str, rows: int, cols: int):
-        if c is None:
-            return None
-        if not isinstance(c, Act8):
-            raise TypeError(f"{name}: expected an Act8")
-        if (c.rows, c.cols) != (rows, cols):
-            raise ValueError(f"{name}: holds {c.rows} x {c.cols}, expected {rows} x {cols}")
-        self._on(c.buf, name)
-        _need(c.buf, torch.uint8, name)
-        if c.buf.numel() < zero_act8_bytes(rows, cols):
-            raise ValueError(f"{name}: {c.buf.numel()} bytes for {rows} x {cols}")
-        return c.buf.data_ptr()
 
-    def ws(self, ws):
-        if ws is not None:
-            _need_ws(ws)
-            self._on(ws, "ws")
-        return _ptr(ws), _need_ws(ws)
+def _row_major(t, name: str, rows: int, cols: int, dev: int, only=None):
+    """A row-major matrix of any row stride (a vector is one row) as the
+    fields of a zero_rows. None: absent."""
+    if t is None:
+        return _ABSENT
+    _on(t, name, dev)
+    dtype = t.dtype
+    if dtype not in _DTYPES or (only is not None and dtype is not only):
+        raise TypeError(f"{name}: expected {only or 'torch.bfloat16 or torch.float32'}, got {dtype}")
+    dim = t.dim()
+    if dim == 2:
+        r, c = t.shape
+        ld, step = t.stride()
+    elif dim == 1:
+        r, (c,), ld, (step,) = 1, t.shape, 0, t.stride()
+    else:
+        r = None
+    if r != rows or c != cols:
+        raise ValueError(f"{name}: expected {(rows, cols)}, got {tuple(t.shape)}")
+    if c > 1 and step != 1:
+        raise ValueError(f"{name}: the elements of a row must lie next to each other")
+    if r <= 1:
+        ld = c
+    elif ld < c:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), ld, _DTYPES[dtype], 0
+
+
+def _per_row(t, name: str, rows: int, dev: int) -> int:
+    if t is None:
+        return 0
+    _on(t, name, dev)
+    _need(t, torch.float32, name, rows)
+    return t.data_ptr()
+
+
+def _act8(c, name: str, rows: int, cols: int, dev: int) -> int:
+    if c is None:
+        return 0
+    if not isinstance(c, Act8):
+        raise TypeError(f"{name}: expected an Act8")
+    if c.rows != rows or c.cols != cols:
+        raise ValueError(f"{name}: holds {c.rows} x {c.cols}, expected {rows} x {cols}")
+    _on(c.buf, name, dev)
+    _need(c.buf, torch.uint8, name)
+    blocks = -(-cols // 32)
+    if c.buf.numel() < rows * blocks * 33:
+        raise ValueError(f"{name}: {c.buf.numel()} bytes for {rows} x {cols}")
+    return c.buf.data_ptr()
+
+
+def _workspace_of(ws, dev: int):
+    if ws is None:
+        return None, 0
+    n = _need_ws(ws)
+    _on(ws, "ws", dev)
+    return ws.data_ptr(), n
 
 
 def _matrix_shape(t, name: str):
@@ -981,23 +1010,27 @@ def _matrix_shape(t, name: str):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
-    return int(t.shape[0]), int(t.shape[1])
+    return t.shape
+
+
+def _stream_of(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
 
 
 def zero_act8_save(x: torch.Tensor, ckpt: Act8, stream=None) -> None:
-    m = _Marshal()
     rows, cols = _matrix_shape(x, "x")
-    r = m.rows(x, "x", (rows, cols))
-    _check(lib().zero_act8_save(ctypes.byref(r), rows, cols, int(ckpt.format), m.act8(ckpt, "ckpt", rows, cols),
-                                _stream(stream)), "zero_act8_save")
+    dev = _device_of(x, "x")
+    st = lib().zero_act8_save(_ROWS.pack(*_row_major(x, "x", rows, cols, dev)), rows, cols, int(ckpt.format),
+                              _act8(ckpt, "ckpt", rows, cols, dev), _stream_of(stream, dev))
+    _check(st, "zero_act8_save")
 
 
 def zero_act8_load(ckpt: Act8, out: torch.Tensor, stream=None) -> None:
-    m = _Marshal()
     rows, cols = _matrix_shape(out, "out")
-    r = m.rows(out, "out", (rows, cols))
-    _check(lib().zero_act8_load(m.act8(ckpt, "ckpt", rows, cols), rows, cols, int(ckpt.format), ctypes.byref(r),
-                                _stream(stream)), "zero_act8_load")
+    dev = _device_of(out, "out")
+    st = lib().zero_act8_load(_act8(ckpt, "ckpt", rows, cols, dev), rows, cols, int(ckpt.format),
+                              _ROWS.pack(*_row_major(out, "out", rows, cols, dev)), _stream_of(stream, dev))
+    _check(st, "zero_act8_load")
 
 
 def zero_act8_wgrad_workspace_bytes(rows: int, outs: int, cols: int) -> int:
@@ -1008,16 +1041,15 @@ def zero_act8_wgrad(dy: torch.Tensor, ckpt: Act8, dw: torch.Tensor, flags: int =
                     col_scale: Optional[torch.Tensor] = None, stream=None) -> None:
     """dw (outs x cols, bf16 or fp32) = dy^T times the checkpoint's rows, its
     columns times col_scale; with GRAD_ACCUMULATE added to an fp32 dw."""
-    m = _Marshal()
     rows, outs = _matrix_shape(dy, "dy")
-    cols = int(ckpt.cols)
-    cdy = m.rows(dy, "dy", (rows, outs), (torch.bfloat16,))
-    cdw = m.rows(dw, "dw", (outs, cols))
-    scale = m.rows(col_scale, "col_scale", (1, cols))
-    wsp, wsb = m.ws(ws)
-    _check(lib().zero_act8_wgrad(ctypes.byref(cdy), m.act8(ckpt, "ckpt", rows, cols), rows, outs, cols,
-                                 int(ckpt.format), ctypes.byref(scale) if col_scale is not None else None,
-                                 ctypes.byref(cdw), int(flags), wsp, wsb, _stream(stream)), "zero_act8_wgrad")
+    dev, cols = _device_of(dy, "dy"), int(ckpt.cols)
+    wsp, wsb = _workspace_of(ws, dev)
+    scale = None if col_scale is None else _ROWS.pack(*_row_major(col_scale, "col_scale", 1, cols, dev))
+    st = lib().zero_act8_wgrad(_ROWS.pack(*_row_major(dy, "dy", rows, outs, dev, torch.bfloat16)),
+                               _act8(ckpt, "ckpt", rows, cols, dev), rows, outs, cols, int(ckpt.format), scale,
+                               _ROWS.pack(*_row_major(dw, "dw", outs, cols, dev)), int(flags), wsp, wsb,
+                               _stream_of(stream, dev))
+    _check(st, "zero_act8_wgrad")
 
 
 @dataclasses.dataclass
@@ -1066,11 +1098,11 @@ class BlockNormGrad:
     residual_scale: float = 1.0
 
 
-def _act8_format(*ckpts) -> int:
-    formats = {int(c.format) for c in ckpts if c is not None}
-    if len(formats) > 1:
+def _act8_format(a: Optional[Act8], b: Optional[Act8]) -> int:
+    if a is not None and b is not None and a.format != b.format:
         raise ValueError("ckpt_post and ckpt_pre have different formats")
-    return formats.pop() if formats else 0
+    c = a if a is not None else b
+    return 0 if c is None else int(c.format)
 
 
 def _gates(rows: int, gate_rows: int) -> int:
@@ -1080,17 +1112,17 @@ def _gates(rows: int, gate_rows: int) -> int:
 
 
 def zero_block_norm(b: BlockNorm, stream=None) -> None:
-    m = _Marshal()
     rows, cols = _matrix_shape(b.x, "x")
-    full, one, bf16 = (rows, cols), (1, cols), (torch.bfloat16,)
-    c = _CBlockNorm(rows, cols, int(b.gate_rows), float(b.residual_scale), float(b.eps), m.rows(b.x, "x", full),
-                    m.rows(b.y, "y", full, bf16), m.rows(b.w_post, "w_post", one),
-                    m.rows(b.gate, "gate", (_gates(rows, b.gate_rows), cols)) if b.gate is not None else _CRows(),
-                    m.rows(b.w_pre, "w_pre", one), m.rows(b.x_out, "x_out", full, (b.x.dtype,)),
-                    m.rows(b.h, "h", full, bf16), m.f32(b.rstd_post, "rstd_post", rows),
-                    m.f32(b.rstd_pre, "rstd_pre", rows), m.act8(b.ckpt_post, "ckpt_post", rows, cols),
-                    m.act8(b.ckpt_pre, "ckpt_pre", rows, cols), _act8_format(b.ckpt_post, b.ckpt_pre), 0)
-    _check(lib().zero_block_norm(ctypes.byref(c), _stream(stream)), "zero_block_norm")
+    dev, bf16 = _device_of(b.x, "x"), torch.bfloat16
+    gate = _ABSENT if b.gate is None else _row_major(b.gate, "gate", _gates(rows, b.gate_rows), cols, dev)
+    args = _BLOCK_NORM.pack(
+        rows, cols, b.gate_rows, b.residual_scale, b.eps, *_row_major(b.x, "x", rows, cols, dev),
+        *_row_major(b.y, "y", rows, cols, dev, bf16), *_row_major(b.w_post, "w_post", 1, cols, dev), *gate,
+        *_row_major(b.w_pre, "w_pre", 1, cols, dev), *_row_major(b.x_out, "x_out", rows, cols, dev, b.x.dtype),
+        *_row_major(b.h, "h", rows, cols, dev, bf16), _per_row(b.rstd_post, "rstd_post", rows, dev),
+        _per_row(b.rstd_pre, "rstd_pre", rows, dev), _act8(b.ckpt_post, "ckpt_post", rows, cols, dev),
+        _act8(b.ckpt_pre, "ckpt_pre", rows, cols, dev), _act8_format(b.ckpt_post, b.ckpt_pre), 0)
+    _check(lib().zero_block_norm(args, _stream_of(stream, dev)), "zero_block_norm")
 
 
 def zero_block_norm_grad_workspace_bytes(rows: int, cols: int, gate_rows: int) -> int:
@@ -1099,21 +1131,21 @@ def zero_block_norm_grad_workspace_bytes(rows: int, cols: int, gate_rows: int) -
 
 
 def zero_block_norm_grad(b: BlockNormGrad, flags: int = 0, ws: Optional[torch.Tensor] = None, stream=None) -> None:
-    m = _Marshal()
     rows, cols = _matrix_shape(b.dx, "dx")
-    full, one, bf16, like = (rows, cols), (1, cols), (torch.bfloat16,), (b.dx.dtype,)
-    gates = (_gates(rows, b.gate_rows), cols) if b.gate is not None else (0, cols)
-    c = _CBlockNormGrad(rows, cols, int(b.gate_rows), float(b.residual_scale), m.rows(b.dh, "dh", full, bf16),
-                        m.rows(b.dx_out, "dx_out", full, like), m.rows(b.w_post, "w_post", one),
-                        m.rows(b.gate, "gate", gates), m.rows(b.w_pre, "w_pre", one),
-                        m.rows(b.x_out, "x_out", full, like), m.rows(b.y, "y", full, bf16),
-                        m.act8(b.ckpt_pre, "ckpt_pre", rows, cols), m.act8(b.ckpt_post, "ckpt_post", rows, cols),
-                        m.f32(b.rstd_pre, "rstd_pre", rows), m.f32(b.rstd_post, "rstd_post", rows),
-                        m.rows(b.dx, "dx", full), m.rows(b.dy, "dy", full, bf16), m.rows(b.dw_pre, "dw_pre", one),
-                        m.rows(b.dw_post, "dw_post", one), m.rows(b.dgate, "dgate", gates),
-                        _act8_format(b.ckpt_post, b.ckpt_pre), int(flags))
-    wsp, wsb = m.ws(ws)
-    _check(lib().zero_block_norm_grad(ctypes.byref(c), wsp, wsb, _stream(stream)), "zero_block_norm_grad")
+    dev, bf16, like = _device_of(b.dx, "dx"), torch.bfloat16, b.dx.dtype
+    gates = 0 if b.gate is None else _gates(rows, b.gate_rows)
+    wsp, wsb = _workspace_of(ws, dev)
+    args = _BLOCK_NORM_GRAD.pack(
+        rows, cols, b.gate_rows, b.residual_scale, *_row_major(b.dh, "dh", rows, cols, dev, bf16),
+        *_row_major(b.dx_out, "dx_out", rows, cols, dev, like), *_row_major(b.w_post, "w_post", 1, cols, dev),
+        *_row_major(b.gate, "gate", gates, cols, dev), *_row_major(b.w_pre, "w_pre", 1, cols, dev),
+        *_row_major(b.x_out, "x_out", rows, cols, dev, like), *_row_major(b.y, "y", rows, cols, dev, bf16),
+        _act8(b.ckpt_pre, "ckpt_pre", rows, cols, dev), _act8(b.ckpt_post, "ckpt_post", rows, cols, dev),
+        _per_row(b.rstd_pre, "rstd_pre", rows, dev), _per_row(b.rstd_post, "rstd_post", rows, dev),
+        *_row_major(b.dx, "dx", rows, cols, dev), *_row_major(b.dy, "dy", rows, cols, dev, bf16),
+        *_row_major(b.dw_pre, "dw_pre", 1, cols, dev), *_row_major(b.dw_post, "dw_post", 1, cols, dev),
+        *_row_major(b.dgate, "dgate", gates, cols, dev), _act8_format(b.ckpt_post, b.ckpt_pre), flags)
+    _check(lib().zero_block_norm_grad(args, wsp, wsb, _stream_of(stream, dev)), "zero_block_norm_grad")
 
 
 def zero_workspace_forget(ws: torch.Tensor) -> None:

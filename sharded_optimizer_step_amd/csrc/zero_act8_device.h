@@ -80,6 +80,18 @@ __device__ __forceinline__ void load8_any(const Rows& m, int64_t row, int col, i
     else unpack<false>(load8<false>(m, row, col, n), f);
 }
 
+// The same as loaded, so that the load can be started early.
+__device__ __forceinline__ Raw8<true> load8_any(const Rows& m, int64_t row, int col, int n)
+{
+    if (m.f32) return load8<true>(m, row, col, n);
+    return Raw8<true>{load8<false>(m, row, col, n).v[0], u32x4{}};
+}
+__device__ __forceinline__ void unpack_any(const Raw8<true>& r, bool f32, float (&f)[8])
+{
+    if (f32) unpack<true>(r, f);
+    else unpack<false>(Raw8<false>{r.v[0]}, f);
+}
+
 // Two fp32 values to bf16, nearest even (one instruction on gfx950).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
@@ -210,13 +222,16 @@ __device__ __forceinline__ void decode8(u32x2 codes, uint32_t scale, float (&f)[
     const float unit = act8_unit(scale);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int w = static_cast<int>(codes[h]);
         if constexpr (FMT == ZERO_ACT8_E4M3) {
-            f[4 * h + 0] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * unit;
-            f[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * unit;
-            f[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * unit;
-            f[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * unit;
+            // two codes and their scale an instruction; a NaN scale gives NaN
+            const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes[h], unit, false);
+            const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes[h], unit, true);
+            f[4 * h + 0] = lo.x;
+            f[4 * h + 1] = lo.y;
+            f[4 * h + 2] = hi.x;
+            f[4 * h + 3] = hi.y;
         } else {
+            const int w = static_cast<int>(codes[h]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[4 * h + i] = static_cast<float>((w << (24 - 8 * i)) >> 24) * unit;
         }

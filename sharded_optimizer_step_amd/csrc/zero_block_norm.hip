@@ -11,28 +11,31 @@
 namespace zero {
 namespace {
 
-// Sums over the L lanes of a row of N values at once, in every lane, in a fixed
-// order. Rows wider than a wave meet in LDS: `red` alternates between two
+// Rows of up to 512 columns take a wave each, four to a workgroup; wider ones
+// a workgroup of as many waves as they have 512 columns.
+constexpr int kWaveVecs = 64;
+constexpr int kMaxLanes = 1024;
+
+// Sums of N values at once over the lanes of a row, in every lane, in a fixed
+// order. The waves of a workgroup meet in LDS: `red` alternates between two
 // halves, so one barrier a call is enough.
-template <int L, int N>
-__device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[N][16], int& half)
+template <bool WAVE, int N>
+__device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[N][kMaxLanes / 64], int& half)
 {
 #pragma unroll
     for (int n = 0; n < N; ++n) x[n] = wave_sum(x[n]);
-    if constexpr (L > 64) {
-        constexpr int W = L / 64;
-        const int wave = threadIdx.x / 64;
+    if constexpr (!WAVE) {
+        const int waves = blockDim.x / 64;
         if (threadIdx.x % 64 == 0) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) red[half][n][wave] = x[n];
+            for (int n = 0; n < N; ++n) red[half][n][threadIdx.x / 64] = x[n];
         }
         __syncthreads();
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            float s = red[half][n][0];
+        for (int n = 0; n < N; ++n) x[n] = red[half][n][0];
+        for (int w = 1; w < waves; ++w) {
 #pragma unroll
-            for (int w = 1; w < W; ++w) s += red[half][n][w];
-            x[n] = s;
+            for (int n = 0; n < N; ++n) x[n] += red[half][n][w];
         }
         half ^= 1;
     }
@@ -46,31 +49,46 @@ __device__ __forceinline__ void save8(uint8_t* ckpt, int64_t rows, int64_t pitch
     if ((v & 3) == 0) *(ZERO_G uint8_t*)(ckpt + rows * pitch + scale_at(row, pitch, v)) = static_cast<uint8_t>(c.scale);
 }
 
-constexpr int threads_of(int L) { return L < 256 ? 256 : L; }
-
-template <int L, int V, bool F32>
-__global__ __launch_bounds__(threads_of(L)) void block_norm_kernel(NormArgs a)
+// A lane's first vector and the distance to its next one, and the row of its
+// wave or workgroup.
+template <bool WAVE>
+__device__ __forceinline__ int row_lane() { return WAVE ? threadIdx.x % 64 : threadIdx.x; }
+template <bool WAVE>
+__device__ __forceinline__ int row_lanes() { return WAVE ? 64 : blockDim.x; }
+template <bool WAVE>
+__device__ __forceinline__ int64_t row_slot()
 {
-    constexpr int NT = threads_of(L);
-    constexpr int R = NT / L;  // rows of a workgroup
-    __shared__ float red[2][1][16];
+    return WAVE ? static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : blockIdx.x;
+}
+
+// 1 / sqrt(mean + eps)
+__device__ __forceinline__ float row_rstd(float sum, float inv_cols, float eps) { return 1.0f / sqrtf(fmaf(sum, inv_cols, eps)); }
+
+template <bool WAVE, int V, bool F32>
+__global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(NormArgs a)
+{
+    __shared__ float red[2][1][kMaxLanes / 64];
     int half = 0;
-    const int lane = threadIdx.x % L;
+    const int lane = row_lane<WAVE>(), lanes = row_lanes<WAVE>();
     const int nv = static_cast<int>(act8_pitch(a.cols) / 8);
     const int64_t pitch = 8 * static_cast<int64_t>(nv);
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
-    const bool has_y = a.y.p != nullptr, has_post = a.w_post.p != nullptr, has_pre = a.w_pre.p != nullptr;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * R; base < a.rows; base += static_cast<int64_t>(gridDim.x) * R) {
-        // a wave past the last row has nothing to do and, at R > 1, no barrier to meet
-        const int64_t row = R > 1 ? base + __builtin_amdgcn_readfirstlane(threadIdx.x / L) : base;
-        if (R > 1 && row >= a.rows) break;
+    const bool has_y = a.y.p != nullptr, has_post = a.w_post.p != nullptr, has_gate = a.gate.p != nullptr, has_pre = a.w_pre.p != nullptr;
+    // every wave of a workgroup sees the same rows where there are barriers
+    for (int64_t row = row_slot<WAVE>(); row < a.rows; row += static_cast<int64_t>(gridDim.x) * (WAVE ? 4 : 1)) {
+        const int64_t g = has_gate ? div_by(static_cast<uint32_t>(row), a.gate_div) : 0;
         Raw8<F32> rx[V];
         Raw8<false> ry[V];
+        Raw8<true> post[V], gate[V], pre[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int v = lane + j * L, n = v < nv ? a.cols - 8 * v : 0;
-            rx[j] = load8<F32>(a.x, row, 8 * v, n);
+            const int v = lane + j * lanes, n = v < nv ? a.cols - 8 * v : 0;
             ry[j] = has_y ? load8<false>(a.y, row, 8 * v, n) : Raw8<false>{};
+            rx[j] = load8<F32>(a.x, row, 8 * v, n);
+            if (V > 1) continue;  // the registers do not hold them
+            post[j] = has_post ? load8_any(a.w_post, 0, 8 * v, n) : Raw8<true>{};
+            gate[j] = has_gate ? load8_any(a.gate, g, 8 * v, n) : Raw8<true>{};
+            pre[j] = has_pre ? load8_any(a.w_pre, 0, 8 * v, n) : Raw8<true>{};
         }
         float x[V][8];
 #pragma unroll
@@ -85,34 +103,28 @@ __global__ __launch_bounds__(threads_of(L)) void block_norm_kernel(NormArgs a)
                 for (int j = 0; j < V; ++j)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) s[0] = fmaf(y[j][i], y[j][i], s[0]);
-                row_sum<L, 1>(s, red, half);
-                rstd = 1.0f / sqrtf(s[0] * inv_cols + a.eps);
+                row_sum<WAVE, 1>(s, red, half);
+                rstd = row_rstd(s[0], inv_cols, a.eps);
                 if (a.rstd_post != nullptr && lane == 0) ((ZERO_G float*)a.rstd_post)[row] = rstd;
             }
-            const int64_t g = a.gate.p != nullptr ? div_by(static_cast<uint32_t>(row), a.gate_div) : 0;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int v = lane + j * L, n = a.cols - 8 * v;
+                const int v = lane + j * lanes, n = a.cols - 8 * v;
                 if (v >= nv) continue;
                 float t[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[j][i] *= rstd;
                 if (a.ckpt_post != nullptr) save8(a.ckpt_post, a.rows, pitch, a.format, row, v, y[j]);
                 if (has_post) {
-                    load8_any(a.w_post, 0, 8 * v, n, t);
+                    if (V > 1) post[j] = load8_any(a.w_post, 0, 8 * v, n);
+                    unpack_any(post[j], a.w_post.f32, t);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) y[j][i] *= t[i];
                 }
-                if (a.gate.p != nullptr) {
-                    load8_any(a.gate, g, 8 * v, n, t);
+                if (V > 1 && has_gate) gate[j] = load8_any(a.gate, g, 8 * v, n);
+                unpack_any(gate[j], a.gate.f32, t);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[j][i] *= a.alpha * t[i];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[j][i] *= a.alpha;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] += y[j][i];
+                for (int i = 0; i < 8; ++i) x[j][i] = fmaf(has_gate ? a.alpha * t[i] : a.alpha, y[j][i], x[j][i]);
                 store8<F32>(a.x_out, row, 8 * v, n, x[j]);
                 // the norm below is that of the residual stream as stored
                 if constexpr (!F32) unpack<false>(Raw8<false>{pack8(x[j])}, x[j]);
@@ -124,18 +136,19 @@ __global__ __launch_bounds__(threads_of(L)) void block_norm_kernel(NormArgs a)
             for (int j = 0; j < V; ++j)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) s[0] = fmaf(x[j][i], x[j][i], s[0]);
-            row_sum<L, 1>(s, red, half);
-            const float rstd = 1.0f / sqrtf(s[0] * inv_cols + a.eps);
+            row_sum<WAVE, 1>(s, red, half);
+            const float rstd = row_rstd(s[0], inv_cols, a.eps);
             if (a.rstd_pre != nullptr && lane == 0) ((ZERO_G float*)a.rstd_pre)[row] = rstd;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int v = lane + j * L, n = a.cols - 8 * v;
+                const int v = lane + j * lanes, n = a.cols - 8 * v;
                 if (v >= nv) continue;
                 float w[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[j][i] *= rstd;
                 if (a.ckpt_pre != nullptr) save8(a.ckpt_pre, a.rows, pitch, a.format, row, v, x[j]);
-                load8_any(a.w_pre, 0, 8 * v, n, w);
+                if (V > 1) pre[j] = load8_any(a.w_pre, 0, 8 * v, n);
+                unpack_any(pre[j], a.w_pre.f32, w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] *= x[j][i];
                 store8<false>(a.h, row, 8 * v, n, w);
@@ -162,7 +175,7 @@ __device__ __forceinline__ void grad8(const Rows& m, int64_t row, int col, int n
     }
 }
 
-// What a lane holds of one vector of a row between its two passes over it.
+// What a lane reads of a row.
 // CODED: both saved rows are act8 buffers; otherwise either may be the rows
 // themselves.
 template <bool F32, bool CODED>
@@ -173,6 +186,7 @@ struct GradRow {
     Raw8<false> y;
     u32x2 cx, cy;
     uint32_t sx, sy;
+    float rstd_pre, rstd_post;
 };
 
 // Which operands a call has; all of it is uniform.
@@ -185,6 +199,8 @@ __device__ __forceinline__ GradRow<F32, CODED> load_row(const NormGradArgs& a, c
                                                         int v, int n)
 {
     GradRow<F32, CODED> r{};
+    r.rstd_pre = has.pre ? ((const ZERO_G float*)a.rstd_pre)[row] : 1.0f;
+    r.rstd_post = has.post ? ((const ZERO_G float*)a.rstd_post)[row] : 1.0f;
     if (has.dx_out) r.d = load8<F32>(a.dx_out, row, 8 * v, n);
     if (has.pre) {
         r.h = load8<false>(a.dh, row, 8 * v, n);
@@ -208,17 +224,6 @@ __device__ __forceinline__ GradRow<F32, CODED> load_row(const NormGradArgs& a, c
         }
     }
     return r;
-}
-
-template <bool F32, bool CODED>
-__device__ __forceinline__ void keep_raw(GradRow<F32, CODED>& r)
-{
-    asm volatile("" : "+v"(r.d.v[0]), "+v"(r.h.v[0]), "+v"(r.cx), "+v"(r.cy), "+v"(r.sx), "+v"(r.sy));
-    if constexpr (F32) asm volatile("" : "+v"(r.d.v[1]));
-    if constexpr (!CODED) {
-        asm volatile("" : "+v"(r.x.v[0]), "+v"(r.y.v[0]));
-        if constexpr (F32) asm volatile("" : "+v"(r.x.v[1]));
-    }
 }
 
 template <bool F32>
@@ -267,36 +272,44 @@ __device__ __forceinline__ void add_to(float (&sum)[8], const float (&x)[8], con
     for (int i = 0; i < 8; ++i) sum[i] = fmaf(x[i], y[i], sum[i]);
 }
 
+// 8 columns of a row as both passes over it need them.
+struct GradCols {
+    float d[8];   // dx_out + rstd_pre v, v = w_pre dh
+    float xn[8], yn[8];
+};
+
 // With v = w_pre dh, the two row means that the formulas need, mean(v xn) and
 // mean(e d yn) with d = dx_out + rstd (v - xn mean(v xn)), come from three
 // sums that do not wait for each other: sum v xn, sum e yn (dx_out + rstd v)
 // and sum e yn xn. One exchange between the waves a row, not two. This adds 8
-// columns to the three sums.
+// columns to the three sums, and dh xn to sum_pre.
 template <bool F32, bool CODED>
-__device__ __forceinline__ void add_row_sums(const NormGradArgs& a, const GradHas& has, int64_t gate_row, int v, int n,
-                                             const GradRow<F32, CODED>& raw, float rstd_pre, float rstd_post, float (&s)[3])
+__device__ __forceinline__ void add_row_sums(const NormGradArgs& a, const GradHas& has, const GradRow<F32, CODED>& raw,
+                                             const float (&w_pre)[8], const float (&e)[8], GradCols& c, float (&s)[3],
+                                             float (&sum_pre)[8])
 {
-    float d[8], xn[8], w[8], t[8];
-    unpack<F32>(raw.d, d);
+    unpack<F32>(raw.d, c.d);
     if (has.pre) {
-        saved8<F32>(CODED || a.ckpt_pre != nullptr, a.format, raw.cx, raw.sx, raw.x, rstd_pre, xn);
-        unpack<false>(raw.h, t);
-        load8_any(a.w_pre, 0, 8 * v, n, w);
+        float h[8];
+        saved8<F32>(CODED || a.ckpt_pre != nullptr, a.format, raw.cx, raw.sx, raw.x, raw.rstd_pre, c.xn);
+        unpack<false>(raw.h, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            t[i] *= w[i];
-            s[0] = fmaf(t[i], xn[i], s[0]);
-            d[i] = fmaf(rstd_pre, t[i], d[i]);
+            sum_pre[i] = fmaf(h[i], c.xn[i], sum_pre[i]);
+            const float v = h[i] * w_pre[i];
+            s[0] = fmaf(v, c.xn[i], s[0]);
+            c.d[i] = fmaf(raw.rstd_pre, v, c.d[i]);
         }
     }
-    if (has.post && has.yn) {
-        saved8<false>(CODED || a.ckpt_post != nullptr, a.format, raw.cy, raw.sy, raw.y, rstd_post, t);
-        load_e(a, has, gate_row, v, n, w);
+    if (has.yn) {
+        saved8<false>(CODED || a.ckpt_post != nullptr, a.format, raw.cy, raw.sy, raw.y, raw.rstd_post, c.yn);
+        if (has.post) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float ey = w[i] * t[i];
-            s[1] = fmaf(ey, d[i], s[1]);
-            if (has.pre) s[2] = fmaf(ey, xn[i], s[2]);
+            for (int i = 0; i < 8; ++i) {
+                const float ey = e[i] * c.yn[i];
+                s[1] = fmaf(ey, c.d[i], s[1]);
+                if (has.pre) s[2] = fmaf(ey, c.xn[i], s[2]);
+            }
         }
     }
 }
@@ -313,25 +326,28 @@ __device__ __forceinline__ Along along(const GradHas& has, const float (&s)[3], 
 
 // The row sums alone, for rows too wide for one workgroup's registers.
 template <bool F32, bool CODED>
-__global__ __launch_bounds__(1024) void block_norm_along_kernel(NormGradArgs a)
+__global__ __launch_bounds__(kMaxLanes) void block_norm_along_kernel(NormGradArgs a)
 {
-    __shared__ float red[2][3][16];
+    __shared__ float red[2][3][kMaxLanes / 64];
     int half = 0;
     const GradHas has = grad_has(a);
     const int nv = static_cast<int>(act8_pitch(a.cols) / 8);
     const int64_t pitch = 8 * static_cast<int64_t>(nv);
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const float rstd_pre = has.pre ? ((const ZERO_G float*)a.rstd_pre)[row] : 1.0f;
-        const float rstd_post = has.post ? ((const ZERO_G float*)a.rstd_post)[row] : 1.0f;
         const int64_t gate_row = has.gate ? div_by(static_cast<uint32_t>(row), a.gate_div) : 0;
-        float s[3] = {0.0f, 0.0f, 0.0f};
-        for (int v = threadIdx.x; v < nv; v += 1024) {
+        float s[3] = {0.0f, 0.0f, 0.0f}, unused[8] = {}, rstd_pre = 1.0f;
+        for (int v = threadIdx.x; v < nv; v += kMaxLanes) {
             const int n = a.cols - 8 * v;
             const GradRow<F32, CODED> raw = load_row<F32, CODED>(a, has, pitch, row, v, n);
-            add_row_sums<F32, CODED>(a, has, gate_row, v, n, raw, rstd_pre, rstd_post, s);
+            float w[8] = {}, e[8];
+            if (has.pre) load8_any(a.w_pre, 0, 8 * v, n, w);
+            load_e(a, has, gate_row, v, n, e);
+            GradCols c;
+            add_row_sums<F32, CODED>(a, has, raw, w, e, c, s, unused);
+            rstd_pre = raw.rstd_pre;
         }
-        row_sum<1024, 3>(s, red, half);
+        row_sum<false, 3>(s, red, half);
         if (threadIdx.x == 0) {
             const Along r = along(has, s, rstd_pre, inv_cols);
             ((ZERO_G float*)a.row_sums)[2 * row] = r.x;
@@ -340,28 +356,30 @@ __global__ __launch_bounds__(1024) void block_norm_along_kernel(NormGradArgs a)
     }
 }
 
+// A lane keeps 8 columns: their weights and their column sums in registers
+// over all rows of its unit. The next row's loads are started before this
+// row's sums, so they are in flight across its barrier.
+//
 // MANY: a unit takes many whole gate rows; dgate is written as each of them
 // ends. Otherwise a unit lies in one gate row and its sums of d yn go to the
 // workspace, from which the join takes both dgate and dw_post.
 //
-// A lane keeps its part of a row as loaded, not as fp32, from the sums to the
-// results, and unpacks it a second time there: the column sums need the
-// registers (keep_raw hides from the compiler that it could keep the fp32).
-//
 // STRIP: the row sums come from block_norm_along_kernel, and a workgroup takes
-// one strip (blockIdx.y) of L * V vectors of its unit's rows.
-template <int L, int V, bool F32, bool CODED, bool MANY, bool STRIP>
-__global__ __launch_bounds__(threads_of(L)) void block_norm_grad_kernel(NormGradArgs a)
+// one strip (blockIdx.y) of its unit's columns.
+//
+// MAX: the most threads of a workgroup. Those of more than 512 have 128
+// registers each, and do without the early loads.
+template <bool WAVE, int MAX, bool F32, bool CODED, bool MANY, bool STRIP>
+__global__ __launch_bounds__(MAX) void block_norm_grad_kernel(NormGradArgs a)
 {
-    constexpr int NT = threads_of(L);
-    constexpr int R = NT / L;
-    __shared__ float red[2][3][16];
+    __shared__ float red[2][3][kMaxLanes / 64];
     int half = 0;
-    const int lane = threadIdx.x % L + (STRIP ? static_cast<int>(blockIdx.y) * L * V : 0);
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * R + (R > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / L) : 0);
-    if (unit >= a.plan.units) return;  // whole waves at R > 1, no one at R == 1
+    const int v = row_lane<WAVE>() + (STRIP ? static_cast<int>(blockIdx.y * blockDim.x) : 0);
+    const int64_t unit = row_slot<WAVE>();
+    if (unit >= a.plan.units) return;  // whole waves, and none where there are barriers
     const int nv = static_cast<int>(act8_pitch(a.cols) / 8);
     const int64_t pitch = 8 * static_cast<int64_t>(nv);
+    const int n = v < nv ? a.cols - 8 * v : 0;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
     const GradHas has = grad_has(a);
     int64_t gate_row, row, end;
@@ -374,123 +392,73 @@ __global__ __launch_bounds__(threads_of(L)) void block_norm_grad_kernel(NormGrad
         row = gate_row * a.plan.gate_rows + (unit - gate_row * a.plan.per_gate) * a.plan.unit_rows;
         end = min(min(a.rows, (gate_row + 1) * a.plan.gate_rows), row + a.plan.unit_rows);
     }
-    float sum_pre[V][8] = {}, sum_yn[V][8] = {}, sum_post[MANY ? V : 1][8] = {};
-    while (row < end) {
-        // the rows of this unit that share one gate row
-        const int64_t stop = MANY ? min(end, (gate_row + 1) * a.plan.gate_rows) : end;
-        for (; row < stop; ++row) {
-            const float rstd_pre = has.pre ? ((const ZERO_G float*)a.rstd_pre)[row] : 1.0f;
-            const float rstd_post = has.post ? ((const ZERO_G float*)a.rstd_post)[row] : 1.0f;
-            GradRow<F32, CODED> raw[V];
+    float sum_pre[8] = {}, sum_yn[8] = {}, sum_post[8] = {};
+    float w_pre[8] = {}, e[8];
+    if (has.pre) load8_any(a.w_pre, 0, 8 * v, n, w_pre);
+    load_e(a, has, gate_row, v, n, e);
+    constexpr bool kEarly = MAX <= 512;
+    GradRow<F32, CODED> next{};
+    if (kEarly && row < end) next = load_row<F32, CODED>(a, has, pitch, row, v, n);
+    int64_t gate_end = (gate_row + 1) * a.plan.gate_rows;
+    for (; row < end; ++row) {
+        const GradRow<F32, CODED> raw = kEarly ? next : load_row<F32, CODED>(a, has, pitch, row, v, n);
+        if (kEarly && row + 1 < end) next = load_row<F32, CODED>(a, has, pitch, row + 1, v, n);
+        Along m;
+        if constexpr (STRIP) m = Along{((const ZERO_G float*)a.row_sums)[2 * row], ((const ZERO_G float*)a.row_sums)[2 * row + 1]};
+        GradCols c;
+        float s[3] = {0.0f, 0.0f, 0.0f};
+        add_row_sums<F32, CODED>(a, has, raw, w_pre, e, c, s, sum_pre);
+        if constexpr (!STRIP) {
+            if (has.pre || (has.post && has.yn)) row_sum<WAVE, 3>(s, red, half);
+            m = along(has, s, raw.rstd_pre, inv_cols);
+        }
+        if (v < nv) {
+            if (has.pre) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int v = lane + j * L, n = v < nv ? a.cols - 8 * v : 0;
-                raw[j] = load_row<F32, CODED>(a, has, pitch, row, v, n);
+                for (int i = 0; i < 8; ++i) c.d[i] = fmaf(-m.x, c.xn[i], c.d[i]);
             }
-            Along m;
-            if constexpr (STRIP) {
-                m = Along{((const ZERO_G float*)a.row_sums)[2 * row], ((const ZERO_G float*)a.row_sums)[2 * row + 1]};
-            } else {
-                float s[3] = {0.0f, 0.0f, 0.0f};
+            store8<F32>(a.dx, row, 8 * v, n, c.d);
+            if (has.yn) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int v = lane + j * L, n = v < nv ? a.cols - 8 * v : 0;
-                    add_row_sums<F32, CODED>(a, has, gate_row, v, n, raw[j], rstd_pre, rstd_post, s);
-                    keep_raw(raw[j]);
-                }
-                if (has.pre || (has.post && has.yn)) row_sum<L, 3>(s, red, half);
-                m = along(has, s, rstd_pre, inv_cols);
+                for (int i = 0; i < 8; ++i) sum_yn[i] = fmaf(c.d[i], c.yn[i], sum_yn[i]);
             }
+            if (a.dy.p != nullptr) {
+                float o[8];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int v = lane + j * L, n = a.cols - 8 * v;
-                if (v >= nv) continue;
-                float d[8], t[8], w[8];
-                unpack<F32>(raw[j].d, d);
-                if (has.pre) {
-                    float xn[8];
-                    saved8<F32>(CODED || a.ckpt_pre != nullptr, a.format, raw[j].cx, raw[j].sx, raw[j].x, rstd_pre, xn);
-                    unpack<false>(raw[j].h, t);
-                    add_to(sum_pre[j], t, xn);
-                    load8_any(a.w_pre, 0, 8 * v, n, w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = fmaf(-m.x, xn[i], fmaf(rstd_pre, t[i] * w[i], d[i]));
-                }
-                store8<F32>(a.dx, row, 8 * v, n, d);
-                if (!has.y) continue;
-                load_e(a, has, gate_row, v, n, w);
-                if (has.yn) {
-                    saved8<false>(CODED || a.ckpt_post != nullptr, a.format, raw[j].cy, raw[j].sy, raw[j].y, rstd_post, t);
-                    add_to(sum_yn[j], d, t);
-                }
-                if (a.dy.p == nullptr) continue;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = has.post ? rstd_post * fmaf(-m.y, t[i], w[i] * d[i]) : w[i] * d[i];
-                store8<false>(a.dy, row, 8 * v, n, w);
+                for (int i = 0; i < 8; ++i)
+                    o[i] = has.post ? raw.rstd_post * fmaf(-m.y, c.yn[i], e[i] * c.d[i]) : e[i] * c.d[i];
+                store8<false>(a.dy, row, 8 * v, n, o);
             }
         }
         if constexpr (MANY) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int v = lane + j * L, n = a.cols - 8 * v;
-                if (v >= nv) continue;
+            if (row + 1 == gate_end || row + 1 == end) {
                 float t[8];
                 load8_any(a.gate, gate_row, 8 * v, n, t);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum_yn[j][i] *= a.alpha;
-                add_to(sum_post[j], t, sum_yn[j]);
+                for (int i = 0; i < 8; ++i) {
+                    sum_yn[i] *= a.alpha;
+                    sum_post[i] = fmaf(t[i], sum_yn[i], sum_post[i]);
+                }
                 if (a.dgate.p != nullptr) {
                     if (has.post) {
                         load8_any(a.w_post, 0, 8 * v, n, t);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) sum_yn[j][i] *= t[i];
+                        for (int i = 0; i < 8; ++i) sum_yn[i] *= t[i];
                     }
-                    grad8(a.dgate, gate_row, 8 * v, n, a.accumulate, sum_yn[j]);
+                    grad8(a.dgate, gate_row, 8 * v, n, a.accumulate, sum_yn);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum_yn[j][i] = 0.0f;
+                for (int i = 0; i < 8; ++i) sum_yn[i] = 0.0f;
+                ++gate_row;
+                gate_end += a.plan.gate_rows;
+                if (row + 1 < end) load_e(a, has, gate_row, v, n, e);
             }
-            ++gate_row;
         }
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int v = lane + j * L, n = a.cols - 8 * v;
-        if (v >= nv) continue;
-        const Rows pre{a.sum_pre, a.cols, 1}, post{a.sum_post, a.cols, 1};
-        if (a.dw_pre.p != nullptr) store8<true>(pre, unit, 8 * v, n, sum_pre[j]);
-        if (a.dw_post.p != nullptr || (!MANY && a.dgate.p != nullptr))
-            store8<true>(post, unit, 8 * v, n, MANY ? sum_post[j] : sum_yn[j]);
-    }
-}
-
-// The units' sums joined in order: 64 columns a workgroup, its 16 waves each
-// a sixteenth of the units that are summed together.
-constexpr int kJoinWaves = 16;
-
-// The sum over the waves of a workgroup, lane by lane.
-__device__ __forceinline__ float across_waves(float s, float* lds)
-{
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    __syncthreads();
-    lds[wave * 64 + lane] = s;
-    __syncthreads();
-    s = lds[lane];
-#pragma unroll
-    for (int w = 1; w < kJoinWaves; ++w) s += lds[w * 64 + lane];
-    return s;
-}
-
-__device__ __forceinline__ float join_sum(const float* part, int64_t first, int64_t count, int cols, int col, float* lds)
-{
-    const int wave = threadIdx.x / 64;
-    const int64_t each = (count + kJoinWaves - 1) / kJoinWaves;
-    const int64_t from = first + wave * each, to = min(first + count, from + each);
-    float s = 0.0f;
-    if (col < cols) {
-        for (int64_t u = from; u < to; ++u) s += ((const ZERO_G float*)part)[u * cols + col];
-    }
-    return across_waves(s, lds);
+    if (v >= nv) return;
+    const Rows pre{a.sum_pre, a.cols, 1}, post{a.sum_post, a.cols, 1};
+    if (a.dw_pre.p != nullptr) store8<true>(pre, unit, 8 * v, n, sum_pre);
+    if (a.dw_post.p != nullptr || (!MANY && a.dgate.p != nullptr)) store8<true>(post, unit, 8 * v, n, MANY ? sum_post : sum_yn);
 }
 
 __device__ __forceinline__ float one(const Rows& m, int64_t row, int col)
@@ -508,95 +476,136 @@ __device__ __forceinline__ void grad1(const Rows& m, int64_t row, int col, bool 
     }
 }
 
+// The units' sums joined in order: 64 columns a workgroup, its 16 waves each a
+// sixteenth of the units. blockIdx.y 0 makes dw_pre, 1 dw_post (each unit's
+// sum of d yn times its gate row, or with many gate rows the units' own
+// sums), 2 and on dgate, one gate row a workgroup, or one a wave where there
+// are many.
+constexpr int kJoinWaves = 16;
+
+// How many gate rows a workgroup of the join takes.
+__host__ __device__ inline int64_t join_gates(const NormGradPlan& p) { return p.gates < kJoinWaves ? 1 : kJoinWaves; }
+
+// The sum over the waves of a workgroup, lane by lane.
+__device__ __forceinline__ float across_waves(float s, float* lds)
+{
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    lds[wave * 64 + lane] = s;
+    __syncthreads();
+    s = lds[lane];
+#pragma unroll
+    for (int w = 1; w < kJoinWaves; ++w) s += lds[w * 64 + lane];
+    return s;
+}
+
+// The sum of column col over `count` rows of part, in order, eight loads at a time.
+__device__ __forceinline__ float column_sum(const float* part, int64_t first, int64_t count, int cols, int col)
+{
+    const ZERO_G float* p = (const ZERO_G float*)part + first * cols + col;
+    float s = 0.0f;
+    int64_t u = 0;
+    for (; u + 8 <= count; u += 8) {
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = p[static_cast<int64_t>(i) * cols];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += t[i];
+        p += 8 * static_cast<int64_t>(cols);
+    }
+    for (; u < count; ++u, p += cols) s += *p;
+    return s;
+}
+
 __global__ __launch_bounds__(64 * kJoinWaves) void block_norm_join_kernel(NormGradArgs a)
 {
     __shared__ float lds[64 * kJoinWaves];
     const int col = blockIdx.x * 64 + threadIdx.x % 64;
-    const bool writes = threadIdx.x < 64 && col < a.cols;
-    if (a.dw_pre.p != nullptr) {
-        const float s = join_sum(a.sum_pre, 0, a.plan.units, a.cols, col, lds);
-        if (writes) grad1(a.dw_pre, 0, col, a.accumulate, s);
-    }
-    if (a.plan.per_gate == 0) {
-        if (a.dw_post.p != nullptr) {
-            const float s = join_sum(a.sum_post, 0, a.plan.units, a.cols, col, lds);
-            if (writes) grad1(a.dw_post, 0, col, a.accumulate, s);
+    const int64_t wave = threadIdx.x / 64;
+    const bool reads = col < a.cols, writes = reads && wave == 0;
+    const int64_t per_gate = a.plan.per_gate;
+    if (blockIdx.y >= 2) {
+        const int64_t step = join_gates(a.plan), g0 = (blockIdx.y - 2) * step;
+        float s = 0.0f;
+        if (step > 1) {
+            const int64_t g = g0 + wave;
+            if (!reads || g >= a.plan.gates) return;
+            s = column_sum(a.sum_post, g * per_gate, per_gate, a.cols, col);
+            if (a.w_post.p != nullptr) s *= one(a.w_post, 0, col);
+            grad1(a.dgate, g, col, a.accumulate, a.alpha * s);
+            return;
         }
-    } else if (a.dw_post.p != nullptr || a.dgate.p != nullptr) {
-        const int64_t gates = a.plan.gates, per_gate = a.plan.per_gate;
-        const bool reads = col < a.cols && gates > 0;
-        const float w = reads && a.w_post.p != nullptr ? one(a.w_post, 0, col) : 1.0f;
-        float total = 0.0f;
-        if (gates < kJoinWaves) {
-            for (int64_t g = 0; g < gates; ++g) {
-                const float s = join_sum(a.sum_post, g * per_gate, per_gate, a.cols, col, lds);
-                if (!writes) continue;
-                total += (a.gate.p != nullptr ? one(a.gate, g, col) : 1.0f) * s;
-                if (a.dgate.p != nullptr) grad1(a.dgate, g, col, a.accumulate, a.alpha * w * s);
-            }
+        const int64_t each = (per_gate + kJoinWaves - 1) / kJoinWaves, from = min(per_gate, wave * each);
+        if (reads) s = column_sum(a.sum_post, g0 * per_gate + from, min(each, per_gate - from), a.cols, col);
+        s = across_waves(s, lds);
+        if (!writes) return;
+        if (a.w_post.p != nullptr) s *= one(a.w_post, 0, col);
+        grad1(a.dgate, g0, col, a.accumulate, a.alpha * s);
+        return;
+    }
+    const Rows& dw = blockIdx.y == 0 ? a.dw_pre : a.dw_post;
+    if (dw.p == nullptr) return;
+    const int64_t each = (a.plan.units + kJoinWaves - 1) / kJoinWaves;
+    int64_t u = min(a.plan.units, wave * each);
+    const int64_t to = min(a.plan.units, u + each);
+    float s = 0.0f;
+    if (reads) {
+        if (blockIdx.y == 0 || per_gate == 0) {
+            s = column_sum(blockIdx.y == 0 ? a.sum_pre : a.sum_post, u, to - u, a.cols, col);
         } else {
-            // a gate row a wave
-            const int64_t each = (gates + kJoinWaves - 1) / kJoinWaves, wave = threadIdx.x / 64;
-            if (reads) {
-                for (int64_t g = wave * each; g < min(gates, (wave + 1) * each); ++g) {
-                    float s = 0.0f;
-                    for (int64_t u = 0; u < per_gate; ++u) s += ((const ZERO_G float*)a.sum_post)[(g * per_gate + u) * a.cols + col];
-                    total += one(a.gate, g, col) * s;
-                    if (a.dgate.p != nullptr) grad1(a.dgate, g, col, a.accumulate, a.alpha * w * s);
-                }
+            while (u < to) {  // the part of a gate row's units that is this wave's
+                const int64_t g = u / per_gate, stop = min(to, (g + 1) * per_gate);
+                const float t = column_sum(a.sum_post, u, stop - u, a.cols, col);
+                s = fmaf(a.gate.p != nullptr ? a.alpha * one(a.gate, g, col) : a.alpha, t, s);
+                u = stop;
             }
-            total = across_waves(total, lds);
         }
-        if (writes && a.dw_post.p != nullptr) grad1(a.dw_post, 0, col, a.accumulate, a.alpha * total);
     }
+    s = across_waves(s, lds);
+    if (writes) grad1(dw, 0, col, a.accumulate, s);
 }
 
 }  // namespace
 
-template <int L, int V>
-static void norm_shape(const NormArgs& a, hipStream_t s)
+// Threads of a workgroup that takes a row of nv vectors, V of them a lane.
+static unsigned block_threads(int64_t nv, int per_lane) { return static_cast<unsigned>((nv + 64 * per_lane - 1) / (64 * per_lane) * 64); }
+
+template <bool WAVE, int V>
+static void norm_shape(const NormArgs& a, int64_t nv, hipStream_t s)
 {
-    const int64_t groups = (a.rows + threads_of(L) / L - 1) / (threads_of(L) / L);
+    const int64_t groups = WAVE ? (a.rows + 3) / 4 : a.rows;
     const unsigned grid = static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20);
-    if (a.x.f32) block_norm_kernel<L, V, true><<<grid, threads_of(L), 0, s>>>(a);
-    else block_norm_kernel<L, V, false><<<grid, threads_of(L), 0, s>>>(a);
+    const unsigned threads = WAVE ? 256 : block_threads(nv, V);
+    if (a.x.f32) block_norm_kernel<WAVE, V, true><<<grid, threads, 0, s>>>(a);
+    else block_norm_kernel<WAVE, V, false><<<grid, threads, 0, s>>>(a);
 }
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s)
 {
-    const int nv = static_cast<int>(act8_pitch(a.cols) / 8);
-    if (nv <= 64) norm_shape<64, 1>(a, s);
-    else if (nv <= 128) norm_shape<64, 2>(a, s);
-    else if (nv <= 256) norm_shape<256, 1>(a, s);
-    else if (nv <= 512) norm_shape<256, 2>(a, s);
-    else if (nv <= 1024) norm_shape<512, 2>(a, s);
-    else norm_shape<1024, 2>(a, s);
+    const int64_t nv = act8_pitch(a.cols) / 8;
+    if (nv <= kWaveVecs) norm_shape<true, 1>(a, nv, s);
+    else if (nv <= kMaxLanes) norm_shape<false, 1>(a, nv, s);
+    else norm_shape<false, 2>(a, nv, s);
     return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ the backward pass's plan
 
-// A workgroup's registers hold rows of 8192 columns with their column sums;
-// wider rows go in strips of 4096.
-constexpr int kGradMaxVecs = 1024;
+// Rows wider than 8192 columns go in strips of 4096; with many gate rows, whose
+// sums take more registers, those wider than 4096.
 constexpr int kStripLanes = 512;
-
-static int grad_lanes(int64_t cols)
-{
-    const int64_t nv = act8_pitch(cols) / 8;
-    return nv <= 128 ? 64 : nv <= 256 ? 256 : 512;
-}
 
 NormGradPlan norm_grad_plan(int64_t rows, int64_t cols, int64_t gate_rows)
 {
     NormGradPlan p{};
     const int64_t nv = act8_pitch(cols) / 8;
-    p.strips = nv <= kGradMaxVecs ? 0 : (nv + kStripLanes - 1) / kStripLanes;
     p.gate_rows = gate_rows > 0 && gate_rows < rows ? gate_rows : (rows > 0 ? rows : 1);
     p.gates = (rows + p.gate_rows - 1) / p.gate_rows;
     // 16 waves a compute unit: enough rows in flight, and as few partial rows as that takes
-    int64_t target = static_cast<int64_t>(kComputeUnits) * 16 * 64 / grad_lanes(cols);
-    if (p.strips > 0) target /= p.strips;
+    int64_t target = kComputeUnits * 16 / (nv > 64 ? (nv + 63) / 64 : 1);
+    if (nv > kMaxLanes || (nv > 512 && p.gates >= target)) {
+        p.strips = (nv + kStripLanes - 1) / kStripLanes;
+        target = kComputeUnits * 16 / (p.strips * (kStripLanes / 64));
+    }
     if (p.gates >= target) {
         p.unit_gates = (p.gates + target - 1) / target;
         p.units = (p.gates + p.unit_gates - 1) / p.unit_gates;
@@ -614,46 +623,53 @@ NormGradPlan norm_grad_plan(int64_t rows, int64_t cols, int64_t gate_rows)
     return p;
 }
 
-template <int L, int V, bool STRIP, bool F32, bool CODED>
-static void grad_split(const NormGradArgs& a, hipStream_t s)
+template <bool WAVE, int MAX, bool STRIP, bool F32, bool CODED>
+static void grad_split(const NormGradArgs& a, int64_t nv, hipStream_t s)
 {
-    constexpr int R = threads_of(L) / L;
-    const dim3 grid(static_cast<unsigned>((a.plan.units + R - 1) / R), STRIP ? static_cast<unsigned>(a.plan.strips) : 1);
+    const unsigned groups = static_cast<unsigned>(WAVE ? (a.plan.units + 3) / 4 : a.plan.units);
+    const dim3 grid(groups, STRIP ? static_cast<unsigned>(a.plan.strips) : 1);
+    const unsigned threads = WAVE ? 256 : STRIP ? kStripLanes : block_threads(nv, 1);
     if constexpr (STRIP) {
         const unsigned rows = static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : 1 << 20);
-        block_norm_along_kernel<F32, CODED><<<rows, 1024, 0, s>>>(a);
+        block_norm_along_kernel<F32, CODED><<<rows, kMaxLanes, 0, s>>>(a);
     }
-    if (a.plan.per_gate == 0) block_norm_grad_kernel<L, V, F32, CODED, true, STRIP><<<grid, threads_of(L), 0, s>>>(a);
-    else block_norm_grad_kernel<L, V, F32, CODED, false, STRIP><<<grid, threads_of(L), 0, s>>>(a);
+    if constexpr (MAX <= 512) {
+        if (a.plan.per_gate == 0) {
+            block_norm_grad_kernel<WAVE, MAX, F32, CODED, true, STRIP><<<grid, threads, 0, s>>>(a);
+            return;
+        }
+    }
+    block_norm_grad_kernel<WAVE, MAX, F32, CODED, false, STRIP><<<grid, threads, 0, s>>>(a);
 }
 
-template <int L, int V, bool STRIP>
-static void grad_shape(const NormGradArgs& a, hipStream_t s)
+template <bool WAVE, int MAX, bool STRIP>
+static void grad_shape(const NormGradArgs& a, int64_t nv, hipStream_t s)
 {
     // rows that are not needed are neither coded nor read
     const bool coded = (a.ckpt_pre != nullptr || a.x_out.p == nullptr) && (a.ckpt_post != nullptr || a.y.p == nullptr);
-    if (a.dx.f32 && coded) grad_split<L, V, STRIP, true, true>(a, s);
-    else if (a.dx.f32) grad_split<L, V, STRIP, true, false>(a, s);
-    else if (coded) grad_split<L, V, STRIP, false, true>(a, s);
-    else grad_split<L, V, STRIP, false, false>(a, s);
+    if (a.dx.f32 && coded) grad_split<WAVE, MAX, STRIP, true, true>(a, nv, s);
+    else if (a.dx.f32) grad_split<WAVE, MAX, STRIP, true, false>(a, nv, s);
+    else if (coded) grad_split<WAVE, MAX, STRIP, false, true>(a, nv, s);
+    else grad_split<WAVE, MAX, STRIP, false, false>(a, nv, s);
 }
 
 hipError_t launch_block_norm_grad(const NormGradArgs& a, hipStream_t s)
 {
     if (a.plan.units > 0) {
-        const int nv = static_cast<int>(act8_pitch(a.cols) / 8);
-        if (nv <= 64) grad_shape<64, 1, false>(a, s);
-        else if (nv <= 128) grad_shape<64, 2, false>(a, s);
-        else if (nv <= 256) grad_shape<256, 1, false>(a, s);
-        else if (nv <= 512) grad_shape<512, 1, false>(a, s);
-        else if (nv <= kGradMaxVecs) grad_shape<512, 2, false>(a, s);
-        else grad_shape<kStripLanes, 1, true>(a, s);
+        const int64_t nv = act8_pitch(a.cols) / 8;
+        if (nv <= kWaveVecs) grad_shape<true, 256, false>(a, nv, s);
+        else if (nv <= 512) grad_shape<false, 512, false>(a, nv, s);
+        else if (a.plan.strips == 0) grad_shape<false, kMaxLanes, false>(a, nv, s);
+        else grad_shape<false, kStripLanes, true>(a, nv, s);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (a.dw_pre.p == nullptr && a.dw_post.p == nullptr && (a.dgate.p == nullptr || a.plan.per_gate == 0))
         return hipSuccess;
-    block_norm_join_kernel<<<static_cast<unsigned>((a.cols + 63) / 64), 64 * kJoinWaves, 0, s>>>(a);
+    const int64_t step = join_gates(a.plan);
+    const int64_t gates = a.dgate.p != nullptr && a.plan.per_gate > 0 ? (a.plan.gates + step - 1) / step : 0;
+    const dim3 grid(static_cast<unsigned>((a.cols + 63) / 64), static_cast<unsigned>(2 + gates));
+    block_norm_join_kernel<<<grid, 64 * kJoinWaves, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -174,49 +174,68 @@ def test_norm_grad_refusals():
                                    (100000, 64, 1), (100000, 64, 7), (3000, 16384, 1), (3000, 16384, 0), (511, 4096, 1), (2**31 - 1, 1, 0)])
 def test_grad_workspace_is_two_rows_a_unit(r, c, g):
     n = z.zero_block_norm_grad_workspace_bytes(r, c, g)
-    wide = 8 * r if c > 8192 else 0
+    wide = 8 * r if c > 8192 else 0  # and two values a row
     assert n > wide and (n - wide) % (8 * c) == 0
     units = (n - wide) // (8 * c)
     # never more units than rows (the last gate row counted whole), nor many more than the waves that fill the chip
     assert units <= (-(-r // g) * g if g else r) and units <= 2 * 4096
 
 
-def test_binding_refuses_host_tensors_and_shapes():
+def test_packed_structures_are_the_c_ones():
+    for packed, c in ((z._ROWS, z._CRows), (z._BLOCK_NORM, z._CBlockNorm), (z._BLOCK_NORM_GRAD, z._CBlockNormGrad)):
+        assert packed.size == ctypes.sizeof(c)
+        flat = []
+
+        def walk(cls, at):
+            for f, t in cls._fields_:
+                o = at + getattr(cls, f).offset
+                walk(t, o) if issubclass(t, ctypes.Structure) else flat.append((o, t))
+
+        walk(c, 0)
+        values = [float(i) if t is ctypes.c_double else i for i, (_, t) in enumerate(flat)]
+        image = packed.pack(*values)
+        for (o, t), v in zip(flat, values):
+            got = t.from_buffer_copy(image, o).value
+            assert (got or 0) == v, (c, o)
+
+
+def test_binding_refuses_host_tensors_and_shapes(monkeypatch):
     """What the binding itself checks; the C calls are not reached."""
-    class Any(z._Marshal):
-        def __init__(self):
-            self.device = 0
-
-        def _on(self, t, name):  # as if on the device
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(name)
-
-    m = Any()
     t = torch.zeros(4, 8, dtype=torch.bfloat16)
-    assert m.rows(t, "t", (4, 8)).ld == 8 and m.rows(t[:, :3], "t", (4, 3)).ld == 8 and m.rows(t[0], "t", (1, 8)).ld == 8
-    assert m.rows(None, "t", (4, 8)).data is None
-    with pytest.raises(ValueError, match="expected"):
-        m.rows(t, "t", (4, 9))
-    with pytest.raises(TypeError, match="expected"):
-        m.rows(t, "t", (4, 8), (torch.float32,))
-    with pytest.raises(TypeError, match="expected"):
-        m.rows(t.half(), "t", (4, 8))
-    with pytest.raises(ValueError, match="next to each other"):
-        m.rows(t.t(), "t", (8, 4))
-    with pytest.raises(ValueError, match="overlap"):
-        m.rows(t[0:1].expand(4, 8), "t", (4, 8))
-    with pytest.raises(TypeError):
-        m.act8(t, "c", 4, 8)
-    with pytest.raises(ValueError, match="holds"):
-        m.act8(z.Act8(4, 9, 1, t), "c", 4, 8)
-    real = object.__new__(z._Marshal)
-    real.device = 0
+    for call in (lambda: z.zero_act8_save(t, None), lambda: z.zero_act8_load(None, t),
+                 lambda: z.zero_act8_wgrad(t, z.Act8(4, 8, 1, t), t), lambda: z.zero_block_norm(z.BlockNorm(x=t)),
+                 lambda: z.zero_block_norm_grad(z.BlockNormGrad(dx=t))):
+        with pytest.raises((ValueError, TypeError), match="device tensor"):
+            call()
+    with pytest.raises(TypeError, match="Tensor"):
+        z.zero_act8_save([1.0], None)
+    with pytest.raises(ValueError, match="matrix"):
+        z.zero_act8_save(t[0], None)
     with pytest.raises(ValueError, match="device tensor"):
-        real.rows(t, "t", (4, 8))
+        z._row_major(t, "t", 4, 8, 0)
+    monkeypatch.setattr(z, "_on", lambda t, name, dev: None)  # as if on the device
+    assert z._row_major(None, "t", 4, 8, 0) == (0, 0, 0, 0)
+    assert z._row_major(t, "t", 4, 8, 0) == (t.data_ptr(), 8, 1, 0)
+    assert z._row_major(t[:, :3], "t", 4, 3, 0)[1] == 8 and z._row_major(t[0], "t", 1, 8, 0)[1] == 8
+    assert z._row_major(t[:1, 2:5].float(), "t", 1, 3, 0)[1:] == (3, 2, 0)
+    with pytest.raises(ValueError, match="expected"):
+        z._row_major(t, "t", 4, 9, 0)
+    with pytest.raises(ValueError, match="expected"):
+        z._row_major(t[None], "t", 4, 8, 0)
+    with pytest.raises(TypeError, match="expected"):
+        z._row_major(t, "t", 4, 8, 0, torch.float32)
+    with pytest.raises(TypeError, match="expected"):
+        z._row_major(t.half(), "t", 4, 8, 0)
+    with pytest.raises(ValueError, match="next to each other"):
+        z._row_major(t.t(), "t", 8, 4, 0)
+    with pytest.raises(ValueError, match="overlap"):
+        z._row_major(t[0:1].expand(4, 8), "t", 4, 8, 0)
+    with pytest.raises(TypeError):
+        z._act8(t, "c", 4, 8, 0)
+    with pytest.raises(ValueError, match="holds"):
+        z._act8(z.Act8(4, 9, 1, t), "c", 4, 8, 0)
     with pytest.raises(ValueError, match="formats"):
         z._act8_format(z.Act8(1, 1, 1, t), z.Act8(1, 1, 2, t))
     assert z._act8_format(None, z.Act8(1, 1, 2, t)) == 2 and z._act8_format(None, None) == 0
     with pytest.raises(ValueError, match="gate_rows"):
         z._gates(4, 0)
-    with pytest.raises(ValueError, match="matrix"):
-        z._matrix_shape(t[0], "x")
