@@ -685,7 +685,7 @@ size_t zero_act8_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols)
  * zero_block_norm saves them. dw (outs x cols): bf16 (a gradient replica) or
  * fp32; with ZERO_GRAD_ACCUMULATE in flags, fp32 and added to. rows == 0
  * writes zeros (nothing with ZERO_GRAD_ACCUMULATE). rows, outs < 2^31, cols <=
- * 2^30, and dw has fewer than 2^22 tiles of 128 x 128 (6.8e10 elements).
+ * 2^30, and dw has fewer than 2^20 tiles of 128 x 128 (1.7e10 elements).
  * ws: device workspace of zero_act8_wgrad_workspace_bytes(...) bytes, 16-byte
  * aligned (NULL if that is 0), contents irrelevant on entry and not kept; two
  * calls that share one must not run concurrently.

@@ -55,8 +55,8 @@ bool list_ok(int64_t rows, int64_t cols)
 bool product_ok(int64_t rows, int64_t outs, int64_t cols)
 {
     return rows >= 0 && rows <= kMaxSize && outs >= 0 && outs <= kMaxSize && cols >= 0 && cols <= kMaxCols &&
-           // one workgroup of at most 512 threads for every tile of dw: a grid counts fewer than 2^32 threads
-           ((outs + 127) / 128) * ((cols + 127) / 128) < (int64_t{1} << 22);
+           // a workgroup of 256 threads for every 64 x 64 of dw, at the most: a grid counts fewer than 2^32 threads
+           ((outs + 127) / 128) * ((cols + 127) / 128) < (int64_t{1} << 20);
 }
 
 bool norm_sizes_ok(int64_t rows, int64_t cols)
