@@ -925,25 +925,25 @@ _BLOCK_NORM_GRAD = struct.Struct("=qqqd" + "QqiI" * 7 + "QQQQ" + "QqiI" * 5 + "i
 _ABSENT = (0, 0, 0, 0)
 
 
-def _device_of(t, name: str) -> int:
-    """The current device, which a call's first operand has to be on."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor")
-    dev = torch.cuda.current_device()
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
-    return dev
-
-
 def _on(t, name: str, dev: int):
+    """Refuses what is not a tensor on device dev."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
+
+
+def _matrix(t, name: str):
+    """The shape of a call's first operand, and the current device, which it has to be on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    return *t.shape, torch.cuda.current_device()
 
 
 def _row_major(t, name: str, rows: int, cols: int, dev: int, only=None):
@@ -951,7 +951,8 @@ def _row_major(t, name: str, rows: int, cols: int, dev: int, only=None):
     fields of a zero_rows. None: absent."""
     if t is None:
         return _ABSENT
-    _on(t, name, dev)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on(t, name, dev)
     dtype = t.dtype
     if dtype not in _DTYPES or (only is not None and dtype is not only):
         raise TypeError(f"{name}: expected {only or 'torch.bfloat16 or torch.float32'}, got {dtype}")
@@ -962,10 +963,10 @@ def _row_major(t, name: str, rows: int, cols: int, dev: int, only=None):
     elif dim == 1:
         r, (c,), ld, (step,) = 1, t.shape, 0, t.stride()
     else:
-        r = None
+        r = c = -1
     if r != rows or c != cols:
         raise ValueError(f"{name}: expected {(rows, cols)}, got {tuple(t.shape)}")
-    if c > 1 and step != 1:
+    if step != 1 and c > 1:
         raise ValueError(f"{name}: the elements of a row must lie next to each other")
     if r <= 1:
         ld = c
@@ -977,8 +978,10 @@ def _row_major(t, name: str, rows: int, cols: int, dev: int, only=None):
 def _per_row(t, name: str, rows: int, dev: int) -> int:
     if t is None:
         return 0
-    _on(t, name, dev)
-    _need(t, torch.float32, name, rows)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on(t, name, dev)
+    if t.dtype is not torch.float32 or t.numel() != rows or not t.is_contiguous():
+        _need(t, torch.float32, name, rows)
     return t.data_ptr()
 
 
@@ -989,12 +992,14 @@ def _act8(c, name: str, rows: int, cols: int, dev: int) -> int:
         raise TypeError(f"{name}: expected an Act8")
     if c.rows != rows or c.cols != cols:
         raise ValueError(f"{name}: holds {c.rows} x {c.cols}, expected {rows} x {cols}")
-    _on(c.buf, name, dev)
-    _need(c.buf, torch.uint8, name)
-    blocks = -(-cols // 32)
-    if c.buf.numel() < rows * blocks * 33:
-        raise ValueError(f"{name}: {c.buf.numel()} bytes for {rows} x {cols}")
-    return c.buf.data_ptr()
+    t = c.buf
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on(t, name, dev)
+    if t.dtype is not torch.uint8 or not t.is_contiguous():
+        _need(t, torch.uint8, name)
+    if t.numel() < rows * -(-cols // 32) * 33:
+        raise ValueError(f"{name}: {t.numel()} bytes for {rows} x {cols}")
+    return t.data_ptr()
 
 
 def _workspace_of(ws, dev: int):
@@ -1005,29 +1010,19 @@ def _workspace_of(ws, dev: int):
     return ws.data_ptr(), n
 
 
-def _matrix_shape(t, name: str):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
-    return t.shape
-
-
 def _stream_of(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
 
 
 def zero_act8_save(x: torch.Tensor, ckpt: Act8, stream=None) -> None:
-    rows, cols = _matrix_shape(x, "x")
-    dev = _device_of(x, "x")
+    rows, cols, dev = _matrix(x, "x")
     st = lib().zero_act8_save(_ROWS.pack(*_row_major(x, "x", rows, cols, dev)), rows, cols, int(ckpt.format),
                               _act8(ckpt, "ckpt", rows, cols, dev), _stream_of(stream, dev))
     _check(st, "zero_act8_save")
 
 
 def zero_act8_load(ckpt: Act8, out: torch.Tensor, stream=None) -> None:
-    rows, cols = _matrix_shape(out, "out")
-    dev = _device_of(out, "out")
+    rows, cols, dev = _matrix(out, "out")
     st = lib().zero_act8_load(_act8(ckpt, "ckpt", rows, cols, dev), rows, cols, int(ckpt.format),
                               _ROWS.pack(*_row_major(out, "out", rows, cols, dev)), _stream_of(stream, dev))
     _check(st, "zero_act8_load")
@@ -1041,8 +1036,8 @@ def zero_act8_wgrad(dy: torch.Tensor, ckpt: Act8, dw: torch.Tensor, flags: int =
                     col_scale: Optional[torch.Tensor] = None, stream=None) -> None:
     """dw (outs x cols, bf16 or fp32) = dy^T times the checkpoint's rows, its
     columns times col_scale; with GRAD_ACCUMULATE added to an fp32 dw."""
-    rows, outs = _matrix_shape(dy, "dy")
-    dev, cols = _device_of(dy, "dy"), int(ckpt.cols)
+    rows, outs, dev = _matrix(dy, "dy")
+    cols = int(ckpt.cols)
     wsp, wsb = _workspace_of(ws, dev)
     scale = None if col_scale is None else _ROWS.pack(*_row_major(col_scale, "col_scale", 1, cols, dev))
     st = lib().zero_act8_wgrad(_ROWS.pack(*_row_major(dy, "dy", rows, outs, dev, torch.bfloat16)),
@@ -1112,8 +1107,8 @@ def _gates(rows: int, gate_rows: int) -> int:
 
 
 def zero_block_norm(b: BlockNorm, stream=None) -> None:
-    rows, cols = _matrix_shape(b.x, "x")
-    dev, bf16 = _device_of(b.x, "x"), torch.bfloat16
+    rows, cols, dev = _matrix(b.x, "x")
+    bf16 = torch.bfloat16
     gate = _ABSENT if b.gate is None else _row_major(b.gate, "gate", _gates(rows, b.gate_rows), cols, dev)
     args = _BLOCK_NORM.pack(
         rows, cols, b.gate_rows, b.residual_scale, b.eps, *_row_major(b.x, "x", rows, cols, dev),
@@ -1131,8 +1126,8 @@ def zero_block_norm_grad_workspace_bytes(rows: int, cols: int, gate_rows: int) -
 
 
 def zero_block_norm_grad(b: BlockNormGrad, flags: int = 0, ws: Optional[torch.Tensor] = None, stream=None) -> None:
-    rows, cols = _matrix_shape(b.dx, "dx")
-    dev, bf16, like = _device_of(b.dx, "dx"), torch.bfloat16, b.dx.dtype
+    rows, cols, dev = _matrix(b.dx, "dx")
+    bf16, like = torch.bfloat16, b.dx.dtype
     gates = 0 if b.gate is None else _gates(rows, b.gate_rows)
     wsp, wsb = _workspace_of(ws, dev)
     args = _BLOCK_NORM_GRAD.pack(

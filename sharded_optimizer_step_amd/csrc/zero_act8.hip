@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kActThreads) void act8_save_kernel(Rows x, int64_t 
         const uint32_t i = u * kActThreads + threadIdx.x;
         if (first + i >= total) continue;
         float f[8];
-        unpack<F32>(raw[u], f);
+        unpack<F32>(raw[u], 8 * at[u].v, cols - 8 * at[u].v, f);
         const Code8 c = encode8<FMT>(f);
         *(ZERO_G u32x2*)(codes + code_at(at[u].row, pitch, at[u].v)) = c.codes;
         if ((at[u].v & 3) == 0) *(ZERO_G uint8_t*)(scales + scale_at(at[u].row, pitch, at[u].v)) = static_cast<uint8_t>(c.scale);

@@ -34,62 +34,66 @@ struct Raw8 {
     u32x4 v[F32 ? 2 : 1];
 };
 
-// Eight elements of a row from column col; those from `n` on are zeros and
-// are not read.
+// Where column `col` of a row lies: what all lanes of a row share, and a 32-bit
+// offset (cols < 2^30), which together are one addressing mode.
+template <bool F32>
+__device__ __forceinline__ char* row_at(const Rows& m, int64_t row, int col)
+{
+    constexpr int kSize = F32 ? 4 : 2;
+    return static_cast<char*>(m.p) + row * m.ld * kSize + static_cast<uint32_t>(col) * kSize;
+}
+
+// A row's last vector may have only n < 8 elements. It is read as the 8
+// elements that end with the row, so that its load is like the others and
+// waits for nothing, and moved into place when it is unpacked.
+__device__ __forceinline__ int back(int col, int n) { return n > 0 && n < 8 && col > 0 ? 8 - n : 0; }
+
+// Eight elements of a row from column col, to be unpacked with the same col
+// and n; elements from `n` on are not read.
 template <bool F32>
 __device__ __forceinline__ Raw8<F32> load8(const Rows& m, int64_t row, int col, int n)
 {
     Raw8<F32> r{};
-    if constexpr (F32) {
-        const float* p = static_cast<const float*>(m.p) + row * m.ld + col;
-        if (n >= 8) {
+    const char* p = row_at<F32>(m, row, col - back(col, n));
+    if (n >= 8 || (n > 0 && col > 0)) {
+        if constexpr (F32) {
             r.v[0] = ld16_a4(p);
-            r.v[1] = ld16_a4(p + 4);
+            r.v[1] = ld16_a4(p + 16);
         } else {
-#pragma unroll
-            for (int i = 0; i < 7; ++i)
-                if (i < n) r.v[i / 4][i % 4] = ((const ZERO_G uint32_t*)p)[i];
-        }
-    } else {
-        const uint16_t* p = static_cast<const uint16_t*>(m.p) + row * m.ld + col;
-        if (n >= 8) {
             r.v[0] = ld16_a2(p);
-        } else {
+        }
+    } else if (n > 0) {  // the row has fewer than 8 columns
 #pragma unroll
-            for (int i = 0; i < 7; ++i)
-                if (i < n) r.v[0][i / 2] |= static_cast<uint32_t>(((const ZERO_G uint16_t*)p)[i]) << (16 * (i % 2));
+        for (int i = 0; i < 7; ++i) {
+            if (i >= n) continue;
+            if constexpr (F32) r.v[i / 4][i % 4] = ((const ZERO_G uint32_t*)p)[i];
+            else r.v[0][i / 2] |= static_cast<uint32_t>(((const ZERO_G uint16_t*)p)[i]) << (16 * (i % 2));
         }
     }
     return r;
 }
 
+// What load8 read, as fp32; zeros from element `n` on.
 template <bool F32>
-__device__ __forceinline__ void unpack(const Raw8<F32>& r, float (&f)[8])
+__device__ __forceinline__ void unpack(const Raw8<F32>& r, int col, int n, float (&f)[8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if constexpr (F32) f[i] = __uint_as_float(r.v[i / 4][i % 4]);
         else f[i] = __uint_as_float(i % 2 ? r.v[0][i / 2] & 0xFFFF0000u : r.v[0][i / 2] << 16);
     }
+    for (int k = back(col, n); k > 0; --k) {  // one lane of a row at most
+#pragma unroll
+        for (int i = 0; i < 7; ++i) f[i] = f[i + 1];
+        f[7] = 0.0f;
+    }
 }
 
 // Eight elements of a vector or gate row of either type, as fp32.
 __device__ __forceinline__ void load8_any(const Rows& m, int64_t row, int col, int n, float (&f)[8])
 {
-    if (m.f32) unpack<true>(load8<true>(m, row, col, n), f);
-    else unpack<false>(load8<false>(m, row, col, n), f);
-}
-
-// The same as loaded, so that the load can be started early.
-__device__ __forceinline__ Raw8<true> load8_any(const Rows& m, int64_t row, int col, int n)
-{
-    if (m.f32) return load8<true>(m, row, col, n);
-    return Raw8<true>{load8<false>(m, row, col, n).v[0], u32x4{}};
-}
-__device__ __forceinline__ void unpack_any(const Raw8<true>& r, bool f32, float (&f)[8])
-{
-    if (f32) unpack<true>(r, f);
-    else unpack<false>(Raw8<false>{r.v[0]}, f);
+    if (m.f32) unpack<true>(load8<true>(m, row, col, n), col, n, f);
+    else unpack<false>(load8<false>(m, row, col, n), col, n, f);
 }
 
 // Two fp32 values to bf16, nearest even (one instruction on gfx950).
@@ -104,22 +108,30 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8])
     return u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
 }
 
+// Eight values rounded to bf16, as fp32.
+__device__ __forceinline__ void round_bf16(float (&f)[8])
+{
+    const u32x4 v = pack8(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(i % 2 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+}
+
 // The first n of eight values to p, rounded to bf16 or as they are.
 template <bool F32>
 __device__ __forceinline__ void store8(const Rows& m, int64_t row, int col, int n, const float (&f)[8])
 {
     if constexpr (F32) {
-        float* p = static_cast<float*>(m.p) + row * m.ld + col;
+        char* p = row_at<true>(m, row, col);
         if (n >= 8) {
             st16_a4(p, __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]}));
-            st16_a4(p + 4, __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]}));
+            st16_a4(p + 16, __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]}));
         } else {
 #pragma unroll
             for (int i = 0; i < 7; ++i)
                 if (i < n) ((ZERO_G float*)p)[i] = f[i];
         }
     } else {
-        uint16_t* p = static_cast<uint16_t*>(m.p) + row * m.ld + col;
+        char* p = row_at<false>(m, row, col);
         const u32x4 v = pack8(f);
         if (n >= 8) {
             st16_a2(p, v);
@@ -170,7 +182,8 @@ struct Code8 {
 // |x| order like their values, with inf and NaN above every finite one, so one
 // integer maximum finds both the largest value and whether the block is
 // finite; its exponent field, carried over when its mantissa is above F's,
-// gives the smallest k with max <= F * 2^k without a logarithm.
+// gives the smallest k with max <= F * 2^k without a logarithm. A block that
+// is not finite gets codes 0 and the scale that makes NaN of any code.
 template <int FMT>
 __device__ __forceinline__ Code8 encode8(const float (&x)[8])
 {
@@ -185,7 +198,7 @@ __device__ __forceinline__ Code8 encode8(const float (&x)[8])
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fine ? x[i] * inv : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = x[i] * inv;
     Code8 r;
     if constexpr (FMT == ZERO_ACT8_E4M3) {
         int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
@@ -206,6 +219,7 @@ __device__ __forceinline__ Code8 encode8(const float (&x)[8])
         };
         r.codes = u32x2{bytes(0), bytes(4)};
     }
+    if (!fine) r.codes = u32x2{0, 0};
     r.scale = fine ? static_cast<uint32_t>(k + 127) : 255u;
     return r;
 }
@@ -239,8 +253,8 @@ __device__ __forceinline__ void decode8(u32x2 codes, uint32_t scale, float (&f)[
 }
 
 // Where the 8 columns of vector v (columns 8v ..) of a row lie in an act8 buffer.
-__device__ __forceinline__ int64_t code_at(int64_t row, int64_t pitch, int v) { return row * pitch + 8 * v; }
-__device__ __forceinline__ int64_t scale_at(int64_t row, int64_t pitch, int v) { return row * (pitch / kActBlock) + v / 4; }
+__device__ __forceinline__ int64_t code_at(int64_t row, int64_t pitch, int v) { return row * pitch + static_cast<uint32_t>(8 * v); }
+__device__ __forceinline__ int64_t scale_at(int64_t row, int64_t pitch, int v) { return row * (pitch / kActBlock) + static_cast<uint32_t>(v) / 4; }
 
 __device__ __forceinline__ u32x2 ld_codes(const uint8_t* p) { return *(const ZERO_G u32x2*)p; }
 __device__ __forceinline__ uint32_t ld_scale(const uint8_t* p) { return *(const ZERO_G uint8_t*)p; }

@@ -69,6 +69,7 @@ hipError_t launch_wgrad(const WgradArgs& a, const WgradPlan& plan, int format, h
 
 struct NormArgs {
     int64_t rows;
+    int64_t unit_rows;  // rows that a workgroup (or wave) takes, set at the launch
     int32_t cols;
     float alpha, eps;
     Rows x, y, w_post, gate, w_pre, x_out, h;
@@ -92,7 +93,7 @@ struct NormGradPlan {
     int64_t unit_rows;
     int64_t unit_gates;
     int64_t units;
-    int64_t strips;      // 0: one workgroup takes whole rows; else strips of columns of a unit
+    int64_t strips;      // strips of columns, where rows may be too wide for one workgroup; else 0
     size_t bytes;        // workspace: two fp32 rows of cols per unit; with strips, two fp32 values per row
 };
 NormGradPlan norm_grad_plan(int64_t rows, int64_t cols, int64_t gate_rows);

@@ -11,6 +11,9 @@
 namespace zero {
 namespace {
 
+#ifndef NORM_ROOM
+#define NORM_ROOM 16
+#endif
 // Rows of up to 512 columns take a wave each, four to a workgroup; wider ones
 // a workgroup of as many waves as they have 512 columns.
 constexpr int kWaveVecs = 64;
@@ -64,45 +67,81 @@ __device__ __forceinline__ int64_t row_slot()
 // 1 / sqrt(mean + eps)
 __device__ __forceinline__ float row_rstd(float sum, float inv_cols, float eps) { return 1.0f / sqrtf(fmaf(sum, inv_cols, eps)); }
 
+__device__ __forceinline__ void add_squares(float& s, const float (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+}
+
+// 8 columns of e = alpha * gate * w_post, what the normalised block output is
+// multiplied with; absent operands are ones.
+__device__ __forceinline__ void load_gain(const Rows& gate, const Rows& w_post, float alpha, int64_t gate_row, int v, int n, float (&e)[8])
+{
+    const bool has_gate = gate.p != nullptr, has_post = w_post.p != nullptr;
+    float t[8];
+    if (has_gate) load8_any(gate, gate_row, 8 * v, n, e);
+    if (has_post) load8_any(w_post, 0, 8 * v, n, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        e[i] = has_gate ? alpha * e[i] : alpha;
+        if (has_post) e[i] *= t[i];
+    }
+}
+
+// A workgroup (or wave) takes neighbouring rows, V vectors of 8 columns a
+// lane. At V == 1 a lane keeps its columns' gain and weight in registers, and
+// the next row's loads are started before this row's sums, so that they are in
+// flight across its two barriers; the gain is read again where the gate's row
+// changes.
 template <bool WAVE, int V, bool F32>
 __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(NormArgs a)
 {
+    constexpr bool kEarly = V == 1;
     __shared__ float red[2][1][kMaxLanes / 64];
     int half = 0;
     const int lane = row_lane<WAVE>(), lanes = row_lanes<WAVE>();
     const int nv = static_cast<int>(act8_pitch(a.cols) / 8);
     const int64_t pitch = 8 * static_cast<int64_t>(nv);
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
-    const bool has_y = a.y.p != nullptr, has_post = a.w_post.p != nullptr, has_gate = a.gate.p != nullptr, has_pre = a.w_pre.p != nullptr;
-    // every wave of a workgroup sees the same rows where there are barriers
-    for (int64_t row = row_slot<WAVE>(); row < a.rows; row += static_cast<int64_t>(gridDim.x) * (WAVE ? 4 : 1)) {
-        const int64_t g = has_gate ? div_by(static_cast<uint32_t>(row), a.gate_div) : 0;
-        Raw8<F32> rx[V];
-        Raw8<false> ry[V];
-        Raw8<true> post[V], gate[V], pre[V];
+    const bool has_y = a.y.p != nullptr, has_post = a.w_post.p != nullptr, has_pre = a.w_pre.p != nullptr;
+    int64_t row = row_slot<WAVE>() * a.unit_rows;
+    const int64_t end = min(a.rows, row + a.unit_rows);
+    if (row >= end) return;  // whole waves, and none where there are barriers
+    Raw8<F32> next_x[V];
+    Raw8<false> next_y[V];
+    const auto load = [&](int64_t r) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int v = lane + j * lanes, n = v < nv ? a.cols - 8 * v : 0;
-            ry[j] = has_y ? load8<false>(a.y, row, 8 * v, n) : Raw8<false>{};
-            rx[j] = load8<F32>(a.x, row, 8 * v, n);
-            if (V > 1) continue;  // the registers do not hold them
-            post[j] = has_post ? load8_any(a.w_post, 0, 8 * v, n) : Raw8<true>{};
-            gate[j] = has_gate ? load8_any(a.gate, g, 8 * v, n) : Raw8<true>{};
-            pre[j] = has_pre ? load8_any(a.w_pre, 0, 8 * v, n) : Raw8<true>{};
+            next_y[j] = has_y ? load8<false>(a.y, r, 8 * v, n) : Raw8<false>{};
+            next_x[j] = load8<F32>(a.x, r, 8 * v, n);
         }
-        float x[V][8];
+    };
+    int64_t gate_row = -1;
+    float e[8], w[8];
+    if (kEarly) {
+        load(row);
+        if (has_pre) load8_any(a.w_pre, 0, 8 * lane, lane < nv ? a.cols - 8 * lane : 0, w);
+    }
+    for (; row < end; ++row) {
+        const int64_t g = a.gate.p != nullptr ? div_by(static_cast<uint32_t>(row), a.gate_div) : 0;
+        if (kEarly && has_y && g != gate_row) load_gain(a.gate, a.w_post, a.alpha, g, lane, lane < nv ? a.cols - 8 * lane : 0, e);
+        gate_row = g;
+        if (!kEarly) load(row);
+        float x[V][8], y[V][8];
 #pragma unroll
-        for (int j = 0; j < V; ++j) unpack<F32>(rx[j], x[j]);
+        for (int j = 0; j < V; ++j) {
+            const int v = lane + j * lanes, n = v < nv ? a.cols - 8 * v : 0;
+            unpack<F32>(next_x[j], 8 * v, n, x[j]);
+            unpack<false>(next_y[j], 8 * v, n, y[j]);
+        }
+        if (kEarly && row + 1 < end) load(row + 1);
         if (has_y) {
-            float y[V][8], rstd = 1.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) unpack<false>(ry[j], y[j]);
+            float rstd = 1.0f;
             if (has_post) {
                 float s[1] = {0.0f};
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s[0] = fmaf(y[j][i], y[j][i], s[0]);
+                for (int j = 0; j < V; ++j) add_squares(s[0], y[j]);
                 row_sum<WAVE, 1>(s, red, half);
                 rstd = row_rstd(s[0], inv_cols, a.eps);
                 if (a.rstd_post != nullptr && lane == 0) ((ZERO_G float*)a.rstd_post)[row] = rstd;
@@ -111,31 +150,21 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(Norm
             for (int j = 0; j < V; ++j) {
                 const int v = lane + j * lanes, n = a.cols - 8 * v;
                 if (v >= nv) continue;
-                float t[8];
+                if (!kEarly) load_gain(a.gate, a.w_post, a.alpha, g, v, n, e);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[j][i] *= rstd;
                 if (a.ckpt_post != nullptr) save8(a.ckpt_post, a.rows, pitch, a.format, row, v, y[j]);
-                if (has_post) {
-                    if (V > 1) post[j] = load8_any(a.w_post, 0, 8 * v, n);
-                    unpack_any(post[j], a.w_post.f32, t);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[j][i] *= t[i];
-                }
-                if (V > 1 && has_gate) gate[j] = load8_any(a.gate, g, 8 * v, n);
-                unpack_any(gate[j], a.gate.f32, t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] = fmaf(has_gate ? a.alpha * t[i] : a.alpha, y[j][i], x[j][i]);
+                for (int i = 0; i < 8; ++i) x[j][i] = fmaf(e[i], y[j][i], x[j][i]);
                 store8<F32>(a.x_out, row, 8 * v, n, x[j]);
                 // the norm below is that of the residual stream as stored
-                if constexpr (!F32) unpack<false>(Raw8<false>{pack8(x[j])}, x[j]);
+                if constexpr (!F32) round_bf16(x[j]);
             }
         }
         if (has_pre) {
             float s[1] = {0.0f};
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[0] = fmaf(x[j][i], x[j][i], s[0]);
+            for (int j = 0; j < V; ++j) add_squares(s[0], x[j]);
             row_sum<WAVE, 1>(s, red, half);
             const float rstd = row_rstd(s[0], inv_cols, a.eps);
             if (a.rstd_pre != nullptr && lane == 0) ((ZERO_G float*)a.rstd_pre)[row] = rstd;
@@ -143,15 +172,13 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(Norm
             for (int j = 0; j < V; ++j) {
                 const int v = lane + j * lanes, n = a.cols - 8 * v;
                 if (v >= nv) continue;
-                float w[8];
+                if (!kEarly) load8_any(a.w_pre, 0, 8 * v, n, w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[j][i] *= rstd;
                 if (a.ckpt_pre != nullptr) save8(a.ckpt_pre, a.rows, pitch, a.format, row, v, x[j]);
-                if (V > 1) pre[j] = load8_any(a.w_pre, 0, 8 * v, n);
-                unpack_any(pre[j], a.w_pre.f32, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] *= x[j][i];
-                store8<false>(a.h, row, 8 * v, n, w);
+                for (int i = 0; i < 8; ++i) y[j][i] = x[j][i] * w[i];
+                store8<false>(a.h, row, 8 * v, n, y[j]);
             }
         }
     }
@@ -165,7 +192,7 @@ __device__ __forceinline__ void grad8(const Rows& m, int64_t row, int col, int n
     if (m.f32) {
         if (accumulate) {
             float old[8];
-            unpack<true>(load8<true>(m, row, col, n), old);
+            unpack<true>(load8<true>(m, row, col, n), col, n, old);
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] += old[i];
         }
@@ -227,11 +254,11 @@ __device__ __forceinline__ GradRow<F32, CODED> load_row(const NormGradArgs& a, c
 }
 
 template <bool F32>
-__device__ __forceinline__ void saved8(bool coded, int format, u32x2 codes, uint32_t scale, const Raw8<F32>& raw, float rstd,
-                                       float (&f)[8])
+__device__ __forceinline__ void saved8(bool coded, int format, u32x2 codes, uint32_t scale, const Raw8<F32>& raw, int v, int n,
+                                       float rstd, float (&f)[8])
 {
     if (!coded) {
-        unpack<F32>(raw, f);
+        unpack<F32>(raw, 8 * v, n, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= rstd;
     } else if (format == ZERO_ACT8_E4M3) {
@@ -253,25 +280,6 @@ __device__ __forceinline__ GradHas grad_has(const NormGradArgs& a)
     return has;
 }
 
-// e = gain * w_post of 8 columns, gain = alpha * gate
-__device__ __forceinline__ void load_e(const NormGradArgs& a, const GradHas& has, int64_t gate_row, int v, int n, float (&e)[8])
-{
-    float t[8];
-    if (has.gate) load8_any(a.gate, gate_row, 8 * v, n, e);
-    if (has.post) load8_any(a.w_post, 0, 8 * v, n, t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        e[i] = has.gate ? a.alpha * e[i] : a.alpha;
-        if (has.post) e[i] *= t[i];
-    }
-}
-
-__device__ __forceinline__ void add_to(float (&sum)[8], const float (&x)[8], const float (&y)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = fmaf(x[i], y[i], sum[i]);
-}
-
 // 8 columns of a row as both passes over it need them.
 struct GradCols {
     float d[8];   // dx_out + rstd_pre v, v = w_pre dh
@@ -285,24 +293,24 @@ struct GradCols {
 // columns to the three sums, and dh xn to sum_pre.
 template <bool F32, bool CODED>
 __device__ __forceinline__ void add_row_sums(const NormGradArgs& a, const GradHas& has, const GradRow<F32, CODED>& raw,
-                                             const float (&w_pre)[8], const float (&e)[8], GradCols& c, float (&s)[3],
+                                             int v, int n, const float (&w_pre)[8], const float (&e)[8], GradCols& c, float (&s)[3],
                                              float (&sum_pre)[8])
 {
-    unpack<F32>(raw.d, c.d);
+    unpack<F32>(raw.d, 8 * v, n, c.d);
     if (has.pre) {
         float h[8];
-        saved8<F32>(CODED || a.ckpt_pre != nullptr, a.format, raw.cx, raw.sx, raw.x, raw.rstd_pre, c.xn);
-        unpack<false>(raw.h, h);
+        saved8<F32>(CODED || a.ckpt_pre != nullptr, a.format, raw.cx, raw.sx, raw.x, v, n, raw.rstd_pre, c.xn);
+        unpack<false>(raw.h, 8 * v, n, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             sum_pre[i] = fmaf(h[i], c.xn[i], sum_pre[i]);
-            const float v = h[i] * w_pre[i];
-            s[0] = fmaf(v, c.xn[i], s[0]);
-            c.d[i] = fmaf(raw.rstd_pre, v, c.d[i]);
+            const float t = h[i] * w_pre[i];
+            s[0] = fmaf(t, c.xn[i], s[0]);
+            c.d[i] = fmaf(raw.rstd_pre, t, c.d[i]);
         }
     }
     if (has.yn) {
-        saved8<false>(CODED || a.ckpt_post != nullptr, a.format, raw.cy, raw.sy, raw.y, raw.rstd_post, c.yn);
+        saved8<false>(CODED || a.ckpt_post != nullptr, a.format, raw.cy, raw.sy, raw.y, v, n, raw.rstd_post, c.yn);
         if (has.post) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -342,9 +350,9 @@ __global__ __launch_bounds__(kMaxLanes) void block_norm_along_kernel(NormGradArg
             const GradRow<F32, CODED> raw = load_row<F32, CODED>(a, has, pitch, row, v, n);
             float w[8] = {}, e[8];
             if (has.pre) load8_any(a.w_pre, 0, 8 * v, n, w);
-            load_e(a, has, gate_row, v, n, e);
+            load_gain(a.gate, a.w_post, a.alpha, gate_row, v, n, e);
             GradCols c;
-            add_row_sums<F32, CODED>(a, has, raw, w, e, c, s, unused);
+            add_row_sums<F32, CODED>(a, has, raw, v, n, w, e, c, s, unused);
             rstd_pre = raw.rstd_pre;
         }
         row_sum<false, 3>(s, red, half);
@@ -367,8 +375,8 @@ __global__ __launch_bounds__(kMaxLanes) void block_norm_along_kernel(NormGradArg
 // STRIP: the row sums come from block_norm_along_kernel, and a workgroup takes
 // one strip (blockIdx.y) of its unit's columns.
 //
-// MAX: the most threads of a workgroup. Those of more than 512 have 128
-// registers each, and do without the early loads.
+// MAX: the most threads of a workgroup. Those of 1024 have 128 registers each,
+// and those of 768 have 168: some of them do without the early loads.
 template <bool WAVE, int MAX, bool F32, bool CODED, bool MANY, bool STRIP>
 __global__ __launch_bounds__(MAX) void block_norm_grad_kernel(NormGradArgs a)
 {
@@ -392,11 +400,11 @@ __global__ __launch_bounds__(MAX) void block_norm_grad_kernel(NormGradArgs a)
         row = gate_row * a.plan.gate_rows + (unit - gate_row * a.plan.per_gate) * a.plan.unit_rows;
         end = min(min(a.rows, (gate_row + 1) * a.plan.gate_rows), row + a.plan.unit_rows);
     }
+    constexpr bool kEarly = MAX < 768 || (MAX == 768 && (CODED || !MANY));
     float sum_pre[8] = {}, sum_yn[8] = {}, sum_post[8] = {};
     float w_pre[8] = {}, e[8];
     if (has.pre) load8_any(a.w_pre, 0, 8 * v, n, w_pre);
-    load_e(a, has, gate_row, v, n, e);
-    constexpr bool kEarly = MAX <= 512;
+    load_gain(a.gate, a.w_post, a.alpha, gate_row, v, n, e);
     GradRow<F32, CODED> next{};
     if (kEarly && row < end) next = load_row<F32, CODED>(a, has, pitch, row, v, n);
     int64_t gate_end = (gate_row + 1) * a.plan.gate_rows;
@@ -407,7 +415,7 @@ __global__ __launch_bounds__(MAX) void block_norm_grad_kernel(NormGradArgs a)
         if constexpr (STRIP) m = Along{((const ZERO_G float*)a.row_sums)[2 * row], ((const ZERO_G float*)a.row_sums)[2 * row + 1]};
         GradCols c;
         float s[3] = {0.0f, 0.0f, 0.0f};
-        add_row_sums<F32, CODED>(a, has, raw, w_pre, e, c, s, sum_pre);
+        add_row_sums<F32, CODED>(a, has, raw, v, n, w_pre, e, c, s, sum_pre);
         if constexpr (!STRIP) {
             if (has.pre || (has.post && has.yn)) row_sum<WAVE, 3>(s, red, half);
             m = along(has, s, raw.rstd_pre, inv_cols);
@@ -451,7 +459,7 @@ __global__ __launch_bounds__(MAX) void block_norm_grad_kernel(NormGradArgs a)
                 for (int i = 0; i < 8; ++i) sum_yn[i] = 0.0f;
                 ++gate_row;
                 gate_end += a.plan.gate_rows;
-                if (row + 1 < end) load_e(a, has, gate_row, v, n, e);
+                if (row + 1 < end) load_gain(a.gate, a.w_post, a.alpha, gate_row, v, n, e);
             }
         }
     }
@@ -569,12 +577,21 @@ __global__ __launch_bounds__(64 * kJoinWaves) void block_norm_join_kernel(NormGr
 // Threads of a workgroup that takes a row of nv vectors, V of them a lane.
 static unsigned block_threads(int64_t nv, int per_lane) { return static_cast<unsigned>((nv + 64 * per_lane - 1) / (64 * per_lane) * 64); }
 
-template <bool WAVE, int V>
-static void norm_shape(const NormArgs& a, int64_t nv, hipStream_t s)
+// Rows of one unit, so that all units together fill the chip once: as many
+// workgroups of `waves` waves a compute unit as `room` waves of it allow.
+static int64_t rows_a_unit(int64_t rows, int64_t waves, int64_t room)
 {
-    const int64_t groups = WAVE ? (a.rows + 3) / 4 : a.rows;
-    const unsigned grid = static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20);
+    const int64_t units = kComputeUnits * (room > waves ? room / waves : 1);
+    return (rows + units - 1) / units;
+}
+
+template <bool WAVE, int V>
+static void norm_shape(NormArgs a, int64_t nv, hipStream_t s)
+{
     const unsigned threads = WAVE ? 256 : block_threads(nv, V);
+    a.unit_rows = rows_a_unit(a.rows, WAVE ? 1 : threads / 64, V == 1 ? NORM_ROOM : 16);
+    const int64_t units = (a.rows + a.unit_rows - 1) / a.unit_rows;
+    const unsigned grid = static_cast<unsigned>(WAVE ? (units + 3) / 4 : units);
     if (a.x.f32) block_norm_kernel<WAVE, V, true><<<grid, threads, 0, s>>>(a);
     else block_norm_kernel<WAVE, V, false><<<grid, threads, 0, s>>>(a);
 }
@@ -590,8 +607,11 @@ hipError_t launch_block_norm(const NormArgs& a, hipStream_t s)
 
 // ------------------------------------------------------------------ the backward pass's plan
 
-// Rows wider than 8192 columns go in strips of 4096; with many gate rows, whose
-// sums take more registers, those wider than 4096.
+// Rows wider than 6144 columns go in strips of 4096, in two passes over them;
+// up to 8192 they still fit one workgroup if they come from 8 bits and there
+// are few gate rows (otherwise its registers do not hold what it needs). The
+// units are the same either way.
+constexpr int kWideVecs = 768;
 constexpr int kStripLanes = 512;
 
 NormGradPlan norm_grad_plan(int64_t rows, int64_t cols, int64_t gate_rows)
@@ -600,11 +620,12 @@ NormGradPlan norm_grad_plan(int64_t rows, int64_t cols, int64_t gate_rows)
     const int64_t nv = act8_pitch(cols) / 8;
     p.gate_rows = gate_rows > 0 && gate_rows < rows ? gate_rows : (rows > 0 ? rows : 1);
     p.gates = (rows + p.gate_rows - 1) / p.gate_rows;
-    // 16 waves a compute unit: enough rows in flight, and as few partial rows as that takes
-    int64_t target = kComputeUnits * 16 / (nv > 64 ? (nv + 63) / 64 : 1);
-    if (nv > kMaxLanes || (nv > 512 && p.gates >= target)) {
+    // as many units as run at once, 16 waves a compute unit, 12 of wide rows
+    const int64_t waves = (nv + 63) / 64;
+    int64_t target = kComputeUnits * (waves > 8 ? 1 : waves > 0 ? 16 / waves : 16);
+    if (nv > kWideVecs) {
         p.strips = (nv + kStripLanes - 1) / kStripLanes;
-        target = kComputeUnits * 16 / (p.strips * (kStripLanes / 64));
+        target = kComputeUnits * 2 / p.strips;
     }
     if (p.gates >= target) {
         p.unit_gates = (p.gates + target - 1) / target;
@@ -633,7 +654,7 @@ static void grad_split(const NormGradArgs& a, int64_t nv, hipStream_t s)
         const unsigned rows = static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : 1 << 20);
         block_norm_along_kernel<F32, CODED><<<rows, kMaxLanes, 0, s>>>(a);
     }
-    if constexpr (MAX <= 512) {
+    if constexpr (MAX < kMaxLanes) {
         if (a.plan.per_gate == 0) {
             block_norm_grad_kernel<WAVE, MAX, F32, CODED, true, STRIP><<<grid, threads, 0, s>>>(a);
             return;
@@ -643,24 +664,30 @@ static void grad_split(const NormGradArgs& a, int64_t nv, hipStream_t s)
 }
 
 template <bool WAVE, int MAX, bool STRIP>
-static void grad_shape(const NormGradArgs& a, int64_t nv, hipStream_t s)
+static void grad_shape(const NormGradArgs& a, bool coded, int64_t nv, hipStream_t s)
 {
-    // rows that are not needed are neither coded nor read
-    const bool coded = (a.ckpt_pre != nullptr || a.x_out.p == nullptr) && (a.ckpt_post != nullptr || a.y.p == nullptr);
-    if (a.dx.f32 && coded) grad_split<WAVE, MAX, STRIP, true, true>(a, nv, s);
-    else if (a.dx.f32) grad_split<WAVE, MAX, STRIP, true, false>(a, nv, s);
-    else if (coded) grad_split<WAVE, MAX, STRIP, false, true>(a, nv, s);
-    else grad_split<WAVE, MAX, STRIP, false, false>(a, nv, s);
+    if constexpr (MAX < kMaxLanes) {
+        if (!coded) {
+            if (a.dx.f32) grad_split<WAVE, MAX, STRIP, true, false>(a, nv, s);
+            else grad_split<WAVE, MAX, STRIP, false, false>(a, nv, s);
+            return;
+        }
+    }
+    if (a.dx.f32) grad_split<WAVE, MAX, STRIP, true, true>(a, nv, s);
+    else grad_split<WAVE, MAX, STRIP, false, true>(a, nv, s);
 }
 
 hipError_t launch_block_norm_grad(const NormGradArgs& a, hipStream_t s)
 {
     if (a.plan.units > 0) {
         const int64_t nv = act8_pitch(a.cols) / 8;
-        if (nv <= kWaveVecs) grad_shape<true, 256, false>(a, nv, s);
-        else if (nv <= 512) grad_shape<false, 512, false>(a, nv, s);
-        else if (a.plan.strips == 0) grad_shape<false, kMaxLanes, false>(a, nv, s);
-        else grad_shape<false, kStripLanes, true>(a, nv, s);
+        // rows that are not needed are neither coded nor read
+        const bool coded = (a.ckpt_pre != nullptr || a.x_out.p == nullptr) && (a.ckpt_post != nullptr || a.y.p == nullptr);
+        if (nv <= kWaveVecs) grad_shape<true, 256, false>(a, coded, nv, s);
+        else if (nv <= 512) grad_shape<false, 512, false>(a, coded, nv, s);
+        else if (nv <= kWideVecs) grad_shape<false, 768, false>(a, coded, nv, s);
+        else if (nv <= kMaxLanes && coded && a.plan.per_gate > 0) grad_shape<false, kMaxLanes, false>(a, coded, nv, s);
+        else grad_shape<false, kStripLanes, true>(a, coded, nv, s);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

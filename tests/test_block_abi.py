@@ -174,7 +174,7 @@ def test_norm_grad_refusals():
                                    (100000, 64, 1), (100000, 64, 7), (3000, 16384, 1), (3000, 16384, 0), (511, 4096, 1), (2**31 - 1, 1, 0)])
 def test_grad_workspace_is_two_rows_a_unit(r, c, g):
     n = z.zero_block_norm_grad_workspace_bytes(r, c, g)
-    wide = 8 * r if c > 8192 else 0  # and two values a row
+    wide = 8 * r if c > 6144 else 0  # and two values a row
     assert n > wide and (n - wide) % (8 * c) == 0
     units = (n - wide) // (8 * c)
     # never more units than rows (the last gate row counted whole), nor many more than the waves that fill the chip
@@ -199,7 +199,7 @@ def test_packed_structures_are_the_c_ones():
             assert (got or 0) == v, (c, o)
 
 
-def test_binding_refuses_host_tensors_and_shapes(monkeypatch):
+def test_binding_refuses_host_tensors_and_shapes():
     """What the binding itself checks; the C calls are not reached."""
     t = torch.zeros(4, 8, dtype=torch.bfloat16)
     for call in (lambda: z.zero_act8_save(t, None), lambda: z.zero_act8_load(None, t),
@@ -213,27 +213,27 @@ def test_binding_refuses_host_tensors_and_shapes(monkeypatch):
         z.zero_act8_save(t[0], None)
     with pytest.raises(ValueError, match="device tensor"):
         z._row_major(t, "t", 4, 8, 0)
-    monkeypatch.setattr(z, "_on", lambda t, name, dev: None)  # as if on the device
-    assert z._row_major(None, "t", 4, 8, 0) == (0, 0, 0, 0)
-    assert z._row_major(t, "t", 4, 8, 0) == (t.data_ptr(), 8, 1, 0)
-    assert z._row_major(t[:, :3], "t", 4, 3, 0)[1] == 8 and z._row_major(t[0], "t", 1, 8, 0)[1] == 8
-    assert z._row_major(t[:1, 2:5].float(), "t", 1, 3, 0)[1:] == (3, 2, 0)
+    # -1 is the host: as if on the device
+    assert z._row_major(None, "t", 4, 8, -1) == (0, 0, 0, 0)
+    assert z._row_major(t, "t", 4, 8, -1) == (t.data_ptr(), 8, 1, 0)
+    assert z._row_major(t[:, :3], "t", 4, 3, -1)[1] == 8 and z._row_major(t[0], "t", 1, 8, -1)[1] == 8
+    assert z._row_major(t[:1, 2:5].float(), "t", 1, 3, -1)[1:] == (3, 2, 0)
     with pytest.raises(ValueError, match="expected"):
-        z._row_major(t, "t", 4, 9, 0)
+        z._row_major(t, "t", 4, 9, -1)
     with pytest.raises(ValueError, match="expected"):
-        z._row_major(t[None], "t", 4, 8, 0)
+        z._row_major(t[None], "t", 4, 8, -1)
     with pytest.raises(TypeError, match="expected"):
-        z._row_major(t, "t", 4, 8, 0, torch.float32)
+        z._row_major(t, "t", 4, 8, -1, torch.float32)
     with pytest.raises(TypeError, match="expected"):
-        z._row_major(t.half(), "t", 4, 8, 0)
+        z._row_major(t.half(), "t", 4, 8, -1)
     with pytest.raises(ValueError, match="next to each other"):
-        z._row_major(t.t(), "t", 8, 4, 0)
+        z._row_major(t.t(), "t", 8, 4, -1)
     with pytest.raises(ValueError, match="overlap"):
-        z._row_major(t[0:1].expand(4, 8), "t", 4, 8, 0)
+        z._row_major(t[0:1].expand(4, 8), "t", 4, 8, -1)
     with pytest.raises(TypeError):
-        z._act8(t, "c", 4, 8, 0)
+        z._act8(t, "c", 4, 8, -1)
     with pytest.raises(ValueError, match="holds"):
-        z._act8(z.Act8(4, 9, 1, t), "c", 4, 8, 0)
+        z._act8(z.Act8(4, 9, 1, t), "c", 4, 8, -1)
     with pytest.raises(ValueError, match="formats"):
         z._act8_format(z.Act8(1, 1, 1, t), z.Act8(1, 1, 2, t))
     assert z._act8_format(None, z.Act8(1, 1, 2, t)) == 2 and z._act8_format(None, None) == 0

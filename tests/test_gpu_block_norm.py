@@ -92,7 +92,7 @@ def check_forward(b, where=""):
 
 
 SIZES = [(1, 1), (2, 7), (3, 8), (5, 31), (1, 32), (7, 33), (65, 64), (3, 511), (4, 513), (130, 768), (3, 1025), (2, 2047),
-         (5, 2049), (3, 4096), (2, 4097), (33, 5003), (2, 8192), (3, 8193), (2, 11008), (2, 16384)]
+         (5, 2049), (3, 4096), (2, 4097), (33, 5003), (3, 6152), (2, 7001), (2, 8192), (3, 8193), (2, 11008), (2, 16384)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
