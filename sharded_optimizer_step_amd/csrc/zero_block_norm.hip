@@ -35,10 +35,10 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[N][kMaxLanes
         }
         __syncthreads();
 #pragma unroll
-        for (int n = 0; n < N; ++n) x[n] = red[half][n][0];
-        for (int w = 1; w < waves; ++w) {
+        for (int n = 0; n < N; ++n) x[n] = 0.0f;
+        for (int w = 0; w < waves; w += 2) {  // in pairs: half the roundings
 #pragma unroll
-            for (int n = 0; n < N; ++n) x[n] += red[half][n][w];
+            for (int n = 0; n < N; ++n) x[n] += red[half][n][w] + (w + 1 < waves ? red[half][n][w + 1] : 0.0f);
         }
         half ^= 1;
     }
@@ -64,8 +64,26 @@ __device__ __forceinline__ int64_t row_slot()
     return WAVE ? static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : blockIdx.x;
 }
 
-// 1 / sqrt(mean + eps)
-__device__ __forceinline__ float row_rstd(float sum, float inv_cols, float eps) { return 1.0f / sqrtf(fmaf(sum, inv_cols, eps)); }
+// 1 / sqrt(sum / cols + eps). The quotient is taken with 1 / cols in two parts
+// and the root refined by one step with an exact residual, which leaves one
+// rounding of each: the 8-bit rows are rounded from what this multiplies, and
+// its error moves some of them to a neighbouring code.
+struct Inverse {
+    float hi, lo;
+};
+__device__ __forceinline__ Inverse inverse(int cols)
+{
+    const float c = static_cast<float>(cols), hi = 1.0f / c;
+    return Inverse{hi, fmaf(-hi, c, 1.0f) * hi};
+}
+__device__ __forceinline__ float row_rstd(float sum, Inverse cols, float eps)
+{
+    const float a = fmaf(sum, cols.hi, fmaf(sum, cols.lo, eps));
+    if (!(a > 0x1p-100f && a < 0x1p100f)) return 1.0f / sqrtf(a);
+    const float r = __builtin_amdgcn_rsqf(a), h = a * r;
+    const float off = fmaf(-h, r, 1.0f) - fmaf(a, r, -h) * r;
+    return fmaf(0.5f * r, off, r);
+}
 
 __device__ __forceinline__ void add_squares(float& s, const float (&x)[8])
 {
@@ -102,7 +120,7 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(Norm
     const int lane = row_lane<WAVE>(), lanes = row_lanes<WAVE>();
     const int nv = static_cast<int>(act8_pitch(a.cols) / 8);
     const int64_t pitch = 8 * static_cast<int64_t>(nv);
-    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    const Inverse inv_cols = inverse(a.cols);
     const bool has_y = a.y.p != nullptr, has_post = a.w_post.p != nullptr, has_pre = a.w_pre.p != nullptr;
     int64_t row = row_slot<WAVE>() * a.unit_rows;
     const int64_t end = min(a.rows, row + a.unit_rows);
