@@ -42,11 +42,13 @@ hipError_t launch_act8_save(const Rows& x, int64_t rows, int64_t cols, int forma
 hipError_t launch_act8_load(const uint8_t* ckpt, int64_t rows, int64_t cols, int format, const Rows& out,
                             hipStream_t s);
 
-// The weight gradient: tiles of dw, each summed over `split` ranges of the
-// rows; with split > 1 the sums go to part[split][outs][cols] and a second
+// The weight gradient: tiles of dw. The first `whole` tiles are summed over all
+// rows by one workgroup; each of the others over `split` ranges of them, whose
+// sums go to the workspace (a tile's ranges next to each other), and a second
 // launch adds them in order.
 struct WgradPlan {
     int tile;       // index of the tile shape
+    int64_t whole;
     int split;      // ranges of rows
     int64_t chunk;  // rows of a range (the last may be shorter)
     size_t bytes;   // workspace

@@ -114,28 +114,41 @@ struct Tile {
     static_assert(NT % CA == 0 && NT % CB == 0 && BK % RA == 0 && BK % RB == 0, "a thread keeps its columns");
 };
 
+// Where tile `id` of a grid of tiles lies: it goes down 8 rows of tiles before
+// it moves a tile to the right, so that neighbours share their factors.
+struct TilePlace {
+    int m, n;
+};
+__host__ __device__ inline TilePlace tile_place(int id, int tiles_m, int tiles_n)
+{
+    constexpr int kDown = 8;
+    const int band = id / (kDown * tiles_n), in_band = id - band * kDown * tiles_n;
+    const int left = tiles_m - band * kDown, rows = left < kDown ? left : kDown;
+    return TilePlace{band * kDown + in_band % rows, in_band / rows};
+}
+
 template <class T, int FMT>
-__global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(WgradArgs a, int tiles_m, int tiles_n, int split, int64_t chunk)
+__global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(WgradArgs a, int tiles_m, int tiles_n, int whole, int split,
+                                                                             int64_t chunk)
 {
     __shared__ __align__(16) uint16_t sa[2][T::BK * T::SA];
     __shared__ __align__(16) uint16_t sb[2][T::BK * T::SB];
-    // Consecutive workgroups go to the eight XCDs in turn: each XCD gets a run
-    // of neighbouring tiles, which share their factors in its L2.
-    const int tiles = tiles_m * tiles_n;
-    const int total = tiles * split;
+    // The first `whole` workgroups take a tile each and all tokens; the tiles
+    // after these are split over the tokens. Consecutive workgroups go to the
+    // eight XCDs in turn: each XCD gets a run of neighbouring tiles, which share
+    // their factors in its L2.
+    const int rest = tiles_m * tiles_n - whole, whole_blocks = (whole + 7) / 8 * 8;
+    const bool parted = static_cast<int>(blockIdx.x) >= whole_blocks;
+    const int block = parted ? blockIdx.x - whole_blocks : blockIdx.x;
+    const int total = parted ? rest * split : whole;
     const int each = (total + 7) / 8;
-    const int id = (blockIdx.x % 8) * each + blockIdx.x / 8;
-    if (id >= total || static_cast<int>(blockIdx.x / 8) >= each) return;
-    const int part = id / tiles;
-    const int in_part = id - part * tiles;
-    // a run of tiles goes down 8 rows of tiles before it moves a tile to the right
-    constexpr int kDown = 8;
-    const int band = in_part / (kDown * tiles_n);
-    const int rows_in_band = min(kDown, tiles_m - band * kDown);
-    const int in_band = in_part - band * kDown * tiles_n;
-    const int64_t m0 = static_cast<int64_t>(band * kDown + in_band % rows_in_band) * T::BM;
-    const int64_t n0 = static_cast<int64_t>(in_band / rows_in_band) * T::BN;
-    const int64_t begin = part * chunk, end = min(a.rows, begin + chunk);
+    const int id = block % 8 * each + block / 8;
+    if (id >= total || block / 8 >= each) return;
+    const int part = parted ? id / rest : 0;
+    const int split_tile = id - part * rest;  // among the split ones
+    const TilePlace place = tile_place(parted ? whole + split_tile : id, tiles_m, tiles_n);
+    const int64_t m0 = static_cast<int64_t>(place.m) * T::BM, n0 = static_cast<int64_t>(place.n) * T::BN;
+    const int64_t begin = parted ? part * chunk : 0, end = parted ? min(a.rows, begin + chunk) : a.rows;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
 
     // This thread's 8 columns of dY. Columns from `outs` on are not read: a
@@ -154,7 +167,7 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(Wg
     const int64_t col_b = n0 + cb < a.pitch ? n0 + cb : 0;
     const int64_t pitch_s = a.pitch / kActBlock;
     // Whole tiles are read at a base that all threads share and 32-bit offsets.
-    const bool plain = !ragged && a.outs >= 8 && a.ld_dy < (int64_t{1} << 24) && a.pitch < (int64_t{1} << 25);
+    const bool plain = a.outs >= 8 && a.ld_dy < (int64_t{1} << 24) && a.pitch < (int64_t{1} << 25);
     uint32_t off_a = static_cast<uint32_t>((row_a * a.ld_dy + col_a) * 2);
     uint32_t off_b = static_cast<uint32_t>(row_b * a.pitch + col_b);
     uint32_t off_s = static_cast<uint32_t>(row_b * pitch_s + col_b / kActBlock);
@@ -195,16 +208,18 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(Wg
         }
     };
     const auto shift_left = [&] {
-        if (ragged && shift > 0) {
+        if (shift == 0) return;
 #pragma unroll
-            for (int i = 0; i < T::VA; ++i) {
-                for (int k = 0; k < shift; ++k) {  // one element to the left
-                    ra[i].x = ra[i].x >> 16 | ra[i].y << 16;
-                    ra[i].y = ra[i].y >> 16 | ra[i].z << 16;
-                    ra[i].z = ra[i].z >> 16 | ra[i].w << 16;
-                    ra[i].w >>= 16;
-                }
+        for (int i = 0; i < T::VA; ++i) {
+            uint64_t lo = ra[i].x | static_cast<uint64_t>(ra[i].y) << 32, hi = ra[i].z | static_cast<uint64_t>(ra[i].w) << 32;
+            if (shift >= 4) {
+                lo = hi >> (16 * (shift - 4));
+                hi = 0;
+            } else {
+                lo = lo >> (16 * shift) | hi << (64 - 16 * shift);
+                hi >>= 16 * shift;
             }
+            ra[i] = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
         }
     };
     const auto stage_whole = [&](int buf) {
@@ -221,7 +236,7 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(Wg
         }
     };
     const auto stage = [&](int buf) {
-        shift_left();
+        if (ragged) shift_left();
         stage_whole(buf);
     };
 
@@ -264,7 +279,7 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(Wg
         __syncthreads();
     };
     const auto whole_step = [&](int64_t k0, int buf) {
-        stage_whole(buf ^ 1);
+        stage(buf ^ 1);
         fetch_whole(k0 + 2 * T::BK);
         multiply(buf);
         __syncthreads();
@@ -297,7 +312,9 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(Wg
     float* out = reinterpret_cast<float*>(&sa[0][0]) + wave * 16 * kPad;
     const int64_t n = n0 + wn + lane % kLanes * 4;
     const int left = n < a.cols ? static_cast<int>(min(a.cols - n, int64_t{4})) : 0;
-    const f32x4 scale = split == 1 ? load_scale(a, n, left) : f32x4{};
+    const f32x4 scale = parted ? f32x4{} : load_scale(a, n, left);
+    // a part of a split tile goes to the workspace whole
+    float* to = a.part + (static_cast<int64_t>(split_tile) * split + part) * (T::BM * T::BN) + wm * T::BN + wn + lane % kLanes * 4;
 #pragma unroll
     for (int i = 0; i < T::TM; ++i) {
 #pragma unroll
@@ -307,70 +324,53 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(Wg
             const int row = r + lane / kLanes;
             const int64_t m = m0 + wm + 16 * i + row;
             const f32x4 v = *reinterpret_cast<const f32x4*>(out + row * kPad + lane % kLanes * 4);
-            if (m >= a.outs || left == 0) continue;
-            if (split == 1) {
-                store_dw(a, m, n, left, v, scale);
-                continue;
-            }
-            float* p = a.part + (static_cast<int64_t>(part) * a.outs + m) * a.cols + n;
-            if (left == 4) st16_a4(p, __builtin_bit_cast(u32x4, v));
-            else {
-#pragma unroll
-                for (int c = 0; c < 3; ++c)
-                    if (c < left) ((ZERO_G float*)p)[c] = v[c];
-            }
+            if (parted) *(ZERO_G f32x4*)(to + (16 * i + row) * T::BN) = v;
+            else if (m < a.outs && left > 0) store_dw(a, m, n, left, v, scale);
         }
     }
 }
 
-// The partial products of a split sum, added in the order of the tokens. A
+// The parts of the split tiles, added in the order of the tokens. A
 // workgroup's eight waves make 8 / waves sets; a set takes 64 vectors of four
-// columns, each of its waves an equal share of the parts, four loads in
-// flight.
+// columns of a tile, each of its waves an equal share of the parts, four loads
+// in flight.
 constexpr int kJoinWaves = 8;
 
 // Four parts a wave before a set gets more waves.
 inline int join_waves(int split) { return split <= 4 ? 1 : split <= 8 ? 2 : split <= 16 ? 4 : kJoinWaves; }
 
-__global__ __launch_bounds__(64 * kJoinWaves) void wgrad_join_kernel(WgradArgs a, int split, int waves, uint32_t per_row, FastDiv by_row)
+// BM x BN tiles, the first of them tile `whole` of the grid.
+template <int BM, int BN>
+__global__ __launch_bounds__(64 * kJoinWaves) void wgrad_join_kernel(WgradArgs a, int tiles_m, int tiles_n, int whole, int split, int waves)
 {
     __shared__ f32x4 sums[kJoinWaves][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int set = wave / waves, member = wave % waves, sets = kJoinWaves / waves;
-    const int64_t size = a.outs * a.cols, vectors = a.outs * per_row;
+    const int set = wave / waves, member = wave % waves;
+    const int tile = blockIdx.y, vector = (static_cast<int>(blockIdx.x) * (kJoinWaves / waves) + set) * 64 + lane;
     const int each = (split + waves - 1) / waves;
     const int from = min(split, member * each), to = min(split, from + each);
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * sets * 64; first < vectors; first += static_cast<int64_t>(gridDim.x) * sets * 64) {
-        const int64_t mine = first + set * 64 + lane, i = min(mine, vectors - 1);
-        const int64_t m = vectors < (1ll << 31) ? div_by(static_cast<uint32_t>(i), by_row) : i / per_row;
-        const int64_t n = (i - m * per_row) * 4;
-        const int left = static_cast<int>(min(a.cols - n, int64_t{4}));
-        const ZERO_G float* p = (const ZERO_G float*)a.part + from * size + m * a.cols + n;
-        f32x4 s{};
-        if (left == 4) {
-            int k = from;
-            for (; k + 4 <= to; k += 4, p += 4 * size) {
-                f32x4 t[4];
+    const ZERO_G f32x4* p = (const ZERO_G f32x4*)a.part + (static_cast<int64_t>(tile) * split + from) * (BM * BN / 4) + vector;
+    f32x4 s{};
+    int k = from;
+    for (; k + 4 <= to; k += 4, p += BM * BN) {
+        f32x4 t[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) t[u] = __builtin_bit_cast(f32x4, ld16_a4((const float*)(p + u * size)));
+        for (int u = 0; u < 4; ++u) t[u] = p[u * (BM * BN / 4)];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) s += t[u];
-            }
-            for (; k < to; ++k, p += size) s += __builtin_bit_cast(f32x4, ld16_a4((const float*)p));
-        } else {
-            for (int k = from; k < to; ++k, p += size)
-#pragma unroll
-                for (int r = 0; r < 3; ++r)
-                    if (r < left) s[r] += p[r];
-        }
-        if (waves > 1) {
-            sums[wave][lane] = s;
-            __syncthreads();
-            for (int w = 1; w < waves; ++w) s += sums[min(wave + w, kJoinWaves - 1)][lane];
-            __syncthreads();
-        }
-        if (member == 0 && mine < vectors) store_dw(a, m, n, left, s, load_scale(a, n, left));
+        for (int u = 0; u < 4; ++u) s += t[u];
     }
+    for (; k < to; ++k, p += BM * BN / 4) s += *p;
+    if (waves > 1) {
+        sums[wave][lane] = s;
+        __syncthreads();
+        if (member != 0) return;
+        for (int w = 1; w < waves; ++w) s += sums[wave + w][lane];
+    }
+    const TilePlace place = tile_place(whole + tile, tiles_m, tiles_n);
+    const int64_t m = static_cast<int64_t>(place.m) * BM + vector / (BN / 4), n = static_cast<int64_t>(place.n) * BN + vector % (BN / 4) * 4;
+    if (m >= a.outs || n >= a.cols) return;
+    const int left = static_cast<int>(min(a.cols - n, int64_t{4}));
+    store_dw(a, m, n, left, s, load_scale(a, n, left));
 }
 
 using TileBig = Tile<256, 256, 32, 2, 4, 1>;
@@ -380,12 +380,16 @@ using TileSmall = Tile<64, 64, 64, 2, 2, 3>;
 template <class T>
 hipError_t launch_tile(const WgradArgs& a, const WgradPlan& plan, int format, hipStream_t s)
 {
-    const int64_t tm = (a.outs + T::BM - 1) / T::BM, tn = (a.cols + T::BN - 1) / T::BN;
-    const int64_t total = tm * tn * plan.split;
-    const unsigned grid = static_cast<unsigned>((total + 7) / 8 * 8);
-    const int m = static_cast<int>(tm), n = static_cast<int>(tn);
-    if (format == ZERO_ACT8_E4M3) wgrad_kernel<T, ZERO_ACT8_E4M3><<<grid, T::NT, 0, s>>>(a, m, n, plan.split, plan.chunk);
-    else wgrad_kernel<T, ZERO_ACT8_INT8><<<grid, T::NT, 0, s>>>(a, m, n, plan.split, plan.chunk);
+    const int m = static_cast<int>((a.outs + T::BM - 1) / T::BM), n = static_cast<int>((a.cols + T::BN - 1) / T::BN);
+    const int whole = static_cast<int>(plan.whole), rest = m * n - whole;
+    const unsigned grid = static_cast<unsigned>((whole + 7) / 8 * 8 + (static_cast<int64_t>(rest) * plan.split + 7) / 8 * 8);
+    if (format == ZERO_ACT8_E4M3) wgrad_kernel<T, ZERO_ACT8_E4M3><<<grid, T::NT, 0, s>>>(a, m, n, whole, plan.split, plan.chunk);
+    else wgrad_kernel<T, ZERO_ACT8_INT8><<<grid, T::NT, 0, s>>>(a, m, n, whole, plan.split, plan.chunk);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || rest == 0 || plan.split == 1) return e;
+    const int waves = join_waves(plan.split);
+    const dim3 join(static_cast<unsigned>(T::BM * T::BN / 4 / 64 * waves / kJoinWaves), static_cast<unsigned>(rest));
+    wgrad_join_kernel<T::BM, T::BN><<<join, 64 * kJoinWaves, 0, s>>>(a, m, n, whole, plan.split, waves);
     return hipGetLastError();
 }
 
@@ -403,38 +407,53 @@ constexpr Candidate candidate(int tile, double alone, double full)
 
 }  // namespace
 
-// The tile and the number of ranges that the tokens are cut into, by the time
-// that they are expected to take: rounds of workgroups through the chip, each
-// of them a start and its tokens, and for a split sum the partial products
-// written, read and joined by a second launch. Measured: 8192 tokens and
-// 4096 x 4096 take 211 us with 256 x 256 tiles, 290 with 128 x 128, 484 with
-// 64 x 64; 1024 tokens and 768 x 768 23, 16 and 9.2 us; 30011 tokens and
-// 200 x 333 unsplit 698, 420 and 218 us, split 30, 26 and 24 us.
+// The tile shape, how many of its tiles are taken whole, and the number of
+// ranges of tokens that the others are cut into, by the time that they are
+// expected to take: rounds of workgroups through the chip, each of them a
+// start and its tokens, and for split tiles their parts written, read and
+// joined by a second launch. Either no tile is whole, or as many as fill whole
+// rounds, or all. Measured: 8192 tokens and 4096 x 4096 take 211 us with
+// 256 x 256 tiles, 290 with 128 x 128, 484 with 64 x 64; 1024 tokens and
+// 768 x 768 23, 16 and 9.2 us; 30011 tokens and 200 x 333 unsplit 698, 420 and
+// 218 us, split 30, 26 and 24 us.
 WgradPlan wgrad_plan(int64_t rows, int64_t outs, int64_t cols)
 {
     static const Candidate kTiles[] = {candidate<TileBig>(0, 0.80, 0.87), candidate<TileMid>(1, 0.95, 1.18),
                                        candidate<TileSmall>(2, 0.47, 0.76)};
-    constexpr double kStart = 4.0, kJoin = 7.0, kBytes = 2e6;  // us a round, us a join, partial bytes written and read a us
+    constexpr double kStart = 4.0, kJoin = 7.0, kBytes = 2e6;  // us a round, us a join, bytes of parts written and read a us
+    constexpr int64_t kMostParts = int64_t{1} << 16;  // tiles of one join (its grid's second size)
     WgradPlan best{};
-    double least = 0.0;
+    double least = -1.0;
     for (const Candidate& c : kTiles) {
         const int64_t tiles = ((outs + c.bm - 1) / c.bm) * ((cols + c.bn - 1) / c.bn);
         const int64_t slots = static_cast<int64_t>(c.slots) * kComputeUnits;
-        for (const int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
-            if (want > 1 && rows < 128 * static_cast<int64_t>(want)) break;
-            int64_t steps = ((rows + want - 1) / want + c.bk - 1) / c.bk;
-            if (steps < 1) steps = 1;
-            const int64_t chunk = steps * c.bk;
-            const int64_t split = rows > 0 ? (rows + chunk - 1) / chunk : 1;
-            const double fill = static_cast<double>(tiles * split) / static_cast<double>(slots);
+        const int64_t all_steps = rows > 0 ? (rows + c.bk - 1) / c.bk : 1;
+        const auto rounds = [&](int64_t groups, int64_t steps) {
+            const double fill = static_cast<double>(groups) / static_cast<double>(slots);
             const double step = c.alone + (c.full - c.alone) * (fill < 1.0 ? fill : 1.0);
-            const double bytes = split > 1 ? 4.0 * static_cast<double>(split) * static_cast<double>(outs) * static_cast<double>(cols) : 0.0;
-            const double us = static_cast<double>((tiles * split + slots - 1) / slots) * (kStart + static_cast<double>(steps) * step) +
-                              (split > 1 ? kJoin + bytes / kBytes : 0.0);
-            if (least == 0.0 || us < least) {
-                least = us;
-                best = WgradPlan{c.tile, static_cast<int>(split), chunk, static_cast<size_t>(bytes)};
+            return static_cast<double>((groups + slots - 1) / slots) * (kStart + static_cast<double>(steps) * step);
+        };
+        const double unsplit = rounds(tiles, all_steps);
+        if (least < 0.0 || unsplit < least) {
+            least = unsplit;
+            best = WgradPlan{c.tile, tiles, 1, all_steps * c.bk, 0};
+        }
+        const int64_t full_rounds = tiles / slots * slots;
+        for (const int64_t whole : {int64_t{0}, full_rounds}) {
+            const int64_t rest = tiles - whole;
+            if (rest == 0 || rest >= kMostParts || (whole == 0 && rest > 2 * slots)) continue;
+            for (const int want : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
+                if (rows < 128 * static_cast<int64_t>(want)) break;
+                const int64_t steps = (all_steps + want - 1) / want;
+                const int64_t split = (all_steps + steps - 1) / steps;
+                const double bytes = 4.0 * static_cast<double>(rest * split) * c.bm * c.bn;
+                const double us = (whole > 0 ? rounds(whole, all_steps) : 0.0) + rounds(rest * split, steps) + kJoin + bytes / kBytes;
+                if (us < least) {
+                    least = us;
+                    best = WgradPlan{c.tile, whole, static_cast<int>(split), steps * c.bk, static_cast<size_t>(bytes)};
+                }
             }
+            if (full_rounds == 0) break;
         }
     }
     return best;
@@ -442,16 +461,9 @@ WgradPlan wgrad_plan(int64_t rows, int64_t outs, int64_t cols)
 
 hipError_t launch_wgrad(const WgradArgs& a, const WgradPlan& plan, int format, hipStream_t s)
 {
-    const hipError_t e = plan.tile == 0   ? launch_tile<TileBig>(a, plan, format, s)
-                         : plan.tile == 1 ? launch_tile<TileMid>(a, plan, format, s)
-                                          : launch_tile<TileSmall>(a, plan, format, s);
-    if (e != hipSuccess || plan.split == 1) return e;
-    const uint32_t per_row = static_cast<uint32_t>((a.cols + 3) / 4);
-    const int waves = join_waves(plan.split);
-    const int64_t each = 64 * kJoinWaves / waves, blocks = (a.outs * per_row + each - 1) / each;
-    const unsigned grid = static_cast<unsigned>(blocks < 8 * kComputeUnits ? blocks : 8 * kComputeUnits);
-    wgrad_join_kernel<<<grid, 64 * kJoinWaves, 0, s>>>(a, plan.split, waves, per_row, fast_div(per_row));
-    return hipGetLastError();
+    return plan.tile == 0   ? launch_tile<TileBig>(a, plan, format, s)
+           : plan.tile == 1 ? launch_tile<TileMid>(a, plan, format, s)
+                            : launch_tile<TileSmall>(a, plan, format, s);
 }
 
 }  // namespace zero

@@ -191,6 +191,20 @@ def test_wgrad_strides_alignments_and_what_lies_beyond(rows, outs, cols, pad, of
     assert canary_ok(buf, outs, cols, pad, offset)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("outs,cols", [(4097, 4097), (4103, 4072)])
+def test_wgrad_of_whole_and_split_tiles(outs, cols, fmt):
+    # more tiles than fit the chip at once: the ones left over are split over the rows
+    rows = 2048
+    n = z.zero_act8_wgrad_workspace_bytes(rows, outs, cols)
+    assert 0 < n < 4 * outs * cols
+    ck, dy, xs = wgrad_case(rows, outs, cols, FORMATS[fmt], 3)
+    for dtype, flags in ((torch.bfloat16, 0), (torch.float32, z.GRAD_ACCUMULATE)):
+        dw = torch.randn(outs, cols, device="cuda", generator=gen(4)).to(dtype)
+        scale = (1 + 0.1 * torch.randn(cols, device="cuda", generator=gen(5))).bfloat16()
+        wgrad_check(ck, dy, xs, dw, flags, scale, dtype)
+
+
 def test_wgrad_of_no_rows_writes_zeros_or_nothing():
     ck = z.new_act8(0, 40, z.ACT8_INT8)
     dy = torch.empty(0, 24, dtype=torch.bfloat16, device="cuda")
