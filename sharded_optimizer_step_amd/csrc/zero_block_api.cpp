@@ -43,6 +43,9 @@ bool optional_ok(const zero_rows& r, int64_t cols, int32_t type, bool vector = f
     return !given(r) || rows_ok(r, cols, type, vector);
 }
 
+// Two outputs of one call at the same address.
+bool same(const void* a, const void* b) { return a != nullptr && a == b; }
+
 Rows view(const zero_rows& r) { return Rows{r.data, r.ld, r.dtype == ZERO_F32}; }
 
 // The vectors of 8 columns that a launch over rows x cols visits have to fit a grid.
@@ -110,7 +113,7 @@ int zero_act8_wgrad(const zero_rows* dy, const void* ckpt, int64_t rows, int64_t
     WgradArgs a{};
     if (col_scale != nullptr) {
         if (!rows_ok(*col_scale, cols, 0, true)) return ZERO_ERR_INVALID_ARGUMENT;
-        a.col_scale = view(*col_scale);
+        if (rows > 0) a.col_scale = view(*col_scale);  // an empty sum is 0 whatever its scale
     }
     const WgradPlan plan = wgrad_plan(rows, outs, cols);
     if (plan.bytes > 0) {
@@ -158,6 +161,8 @@ int zero_block_norm(const zero_block_norm_args* g, hipStream_t stream)
         (g->ckpt_pre != nullptr && !aligned(g->ckpt_pre, kPtrAlign)) ||
         !aligned(g->rstd_post, 4) || !aligned(g->rstd_pre, 4))
         return ZERO_ERR_INVALID_ARGUMENT;
+    if (same(g->x_out.data, g->h.data) || same(g->rstd_post, g->rstd_pre) || same(g->ckpt_post, g->ckpt_pre))
+        return ZERO_ERR_INVALID_ARGUMENT;
     NormArgs a{};
     a.rows = g->rows;
     a.cols = static_cast<int32_t>(g->cols);
@@ -200,6 +205,9 @@ int zero_block_norm_grad(const zero_block_norm_grad_args* g, void* ws, size_t ws
     const int32_t grad_type = accumulate ? ZERO_F32 : 0;
     if (!optional_ok(g->dw_pre, g->cols, grad_type, true) || !optional_ok(g->dw_post, g->cols, grad_type, true) ||
         !optional_ok(g->dgate, g->cols, grad_type))
+        return ZERO_ERR_INVALID_ARGUMENT;
+    if (same(g->dw_pre.data, g->dw_post.data) || same(g->dw_pre.data, g->dgate.data) ||
+        same(g->dw_post.data, g->dgate.data) || same(g->dx.data, g->dy.data))
         return ZERO_ERR_INVALID_ARGUMENT;
     if (g->rows > 0) {
         if (!rows_ok(g->dx, g->cols, 0) || !optional_ok(g->dx_out, g->cols, g->dx.dtype)) return ZERO_ERR_INVALID_ARGUMENT;

@@ -19,14 +19,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 //
 // e4m3: one instruction for two codes and their scale. int8: the code with its
 // sign bit turned over is u = code + 128 in 0 .. 255; under the byte 0x64 it is
-// the half 1024 + u, and one mixed fma makes (1024 + u) unit - 1152 unit =
-// code * unit, without a rounding: two and a quarter instructions a code
-// instead of three and a half.
+// the half 1024 + u, less 1152 the code, and one mixed fma scales it, all
+// without a rounding: two and three quarters instructions a code instead of
+// three and a half. (One fma of 1024 + u with -1152 unit would save half of
+// one, but 1152 unit overflows before the largest blocks do.)
 template <int FMT>
 __device__ __forceinline__ void decode16(u32x4 codes, uint32_t scale, u32x4 (&out)[2])
 {
     const float unit = act8_unit(scale);
-    const float back = -1152.0f * unit;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t lo, hi;
@@ -36,10 +36,11 @@ __device__ __forceinline__ void decode16(u32x4 codes, uint32_t scale, u32x4 (&ou
         } else {
             typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
             const uint32_t u = codes[i] ^ 0x80808080u;
-            const f16x2 a = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u));
-            const f16x2 b = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u));
-            lo = pack_bf16(fmaf(static_cast<float>(a.x), unit, back), fmaf(static_cast<float>(a.y), unit, back));
-            hi = pack_bf16(fmaf(static_cast<float>(b.x), unit, back), fmaf(static_cast<float>(b.y), unit, back));
+            constexpr _Float16 kBack = -1152;
+            const f16x2 a = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) + f16x2{kBack, kBack};
+            const f16x2 b = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) + f16x2{kBack, kBack};
+            lo = pack_bf16(fmaf(static_cast<float>(a.x), unit, 0.0f), fmaf(static_cast<float>(a.y), unit, 0.0f));
+            hi = pack_bf16(fmaf(static_cast<float>(b.x), unit, 0.0f), fmaf(static_cast<float>(b.y), unit, 0.0f));
         }
         out[i / 2][2 * (i % 2)] = lo;
         out[i / 2][2 * (i % 2) + 1] = hi;
@@ -306,7 +307,8 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(Wg
     // of dW, and four lanes 16. Sixteen rows at a time go through LDS (each wave
     // its own part of what the tiles lay in; the last barrier is behind every
     // read of them), so that a store, and a read of what is added to, covers
-    // whole lines.
+    // whole lines. The fences keep the compiler from moving a lane's reads over
+    // its writes, which other lanes read; a wave's LDS accesses are in order.
     constexpr int kWide = T::TN * 16, kLanes = kWide / 4, kPad = kWide + 4;
     static_assert(T::NT / 64 * 16 * kPad * sizeof(float) <= sizeof(sa), "the tiles' LDS holds 16 rows a wave");
     float* out = reinterpret_cast<float*>(&sa[0][0]) + wave * 16 * kPad;
@@ -319,6 +321,7 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(Wg
     for (int i = 0; i < T::TM; ++i) {
 #pragma unroll
         for (int j = 0; j < T::TN; ++j) *reinterpret_cast<f32x4*>(out + lane % 16 * kPad + 16 * j + lane / 16 * 4) = acc[j][i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
         for (int r = 0; r < 16; r += 64 / kLanes) {
             const int row = r + lane / kLanes;
@@ -327,6 +330,7 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void wgrad_kernel(Wg
             if (parted) *(ZERO_G f32x4*)(to + (16 * i + row) * T::BN) = v;
             else if (m < a.outs && left > 0) store_dw(a, m, n, left, v, scale);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
@@ -415,7 +419,8 @@ constexpr Candidate candidate(int tile, double alone, double full)
 // rounds, or all. Measured: 8192 tokens and 4096 x 4096 take 211 us with
 // 256 x 256 tiles, 290 with 128 x 128, 484 with 64 x 64; 1024 tokens and
 // 768 x 768 23, 16 and 9.2 us; 30011 tokens and 200 x 333 unsplit 698, 420 and
-// 218 us, split 30, 26 and 24 us.
+// 218 us, split 30, 26 and 24 us; a million tokens and 64 x 64 78 us in 128
+// ranges, 43 in 768.
 WgradPlan wgrad_plan(int64_t rows, int64_t outs, int64_t cols)
 {
     static const Candidate kTiles[] = {candidate<TileBig>(0, 0.80, 0.87), candidate<TileMid>(1, 0.95, 1.18),
@@ -442,7 +447,7 @@ WgradPlan wgrad_plan(int64_t rows, int64_t outs, int64_t cols)
         for (const int64_t whole : {int64_t{0}, full_rounds}) {
             const int64_t rest = tiles - whole;
             if (rest == 0 || rest >= kMostParts || (whole == 0 && rest > 2 * slots)) continue;
-            for (const int want : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
+            for (const int want : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256, 384, 512, 768}) {
                 if (rows < 128 * static_cast<int64_t>(want)) break;
                 const int64_t steps = (all_steps + want - 1) / want;
                 const int64_t split = (all_steps + steps - 1) / steps;

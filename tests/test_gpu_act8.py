@@ -137,6 +137,22 @@ def test_every_code_and_scale_decodes(fmt):
     assert np.array_equal(dw.double().cpu().numpy(), want[rows])
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,outs,cols", [(70, 40, 96), (300, 300, 300)])
+def test_wgrad_of_the_largest_and_smallest_blocks(rows, outs, cols, fmt):
+    # finite values up to 1.75 * 2^127, and as small as a block's smallest scale
+    # holds: every decoded value is finite, and with dy near 1 / max so are the sums
+    for top, size in ((127, 2.0**-100), (-110, 2.0**60)):
+        sign = torch.sign(randn(rows, cols, 5))
+        mant = 1 + torch.rand(rows, cols, device="cuda", generator=gen(6)) * 0.75
+        x = (sign.double() * mant.double() * 2.0**top).to(torch.float32)
+        ck = save(x, FORMATS[fmt])
+        dy = (torch.randn(rows, outs, device="cuda", generator=gen(7)).double() * size).to(torch.bfloat16)
+        xs = torch.tensor(decode_act8(ck)[0], device="cuda")
+        assert bool(xs.abs().max() < 2.0**128)
+        wgrad_check(ck, dy, xs, torch.empty(outs, cols, device="cuda"), 0, None, (fmt, top))
+
+
 def wgrad_case(rows, outs, cols, fmt, seed, dy_pad=0, dy_offset=0):
     x = randn(rows, cols, seed)
     ck = save(x, fmt)
@@ -211,6 +227,9 @@ def test_wgrad_of_no_rows_writes_zeros_or_nothing():
     for dtype in (torch.bfloat16, torch.float32):
         dw = torch.full((24, 40), 3.0, dtype=dtype, device="cuda")
         z.zero_act8_wgrad(dy, ck, dw)
+        assert torch.equal(dw, torch.zeros_like(dw))
+        dw.fill_(3.0)
+        z.zero_act8_wgrad(dy, ck, dw, col_scale=torch.full((40,), float("inf"), device="cuda"))
         assert torch.equal(dw, torch.zeros_like(dw))
     dw = torch.full((24, 40), 3.0, device="cuda")
     z.zero_act8_wgrad(dy, ck, dw, z.GRAD_ACCUMULATE)
