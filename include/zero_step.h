@@ -51,8 +51,8 @@
  *  - The fused forms launch one workgroup per tile of a pass, at most
  *    2^31 - 1 tiles (an update pass's tiles hold 2048 elements: about 4.4e12
  *    elements per call); a larger call is ZERO_ERR_INVALID_ARGUMENT.
- *  - Outputs must not alias inputs, except the in-place master/exp_avg/
- *    exp_avg_sq. The library never advances `step`: the caller increments it
+ *  - Outputs must not alias inputs or each other, except the in-place
+ *    master/exp_avg/exp_avg_sq and what an entry point allows. The library never advances `step`: the caller increments it
  *    when the result record says `skipped == 0`.
  */
 #ifndef ZERO_STEP_H
@@ -706,7 +706,7 @@ int zero_act8_wgrad(const zero_rows* dy, const void* ckpt, int64_t rows, int64_t
  * w_post (no norm after the block), gate (ones), w_pre (no norm before the
  * next block). rstd_post and rstd_pre (fp32, one per row) are the reciprocal
  * roots; ckpt_post and ckpt_pre the act8 buffers of yn and xn. All sums are
- * fp32; every output is rounded once.
+ * fp32; every output is rounded once. Two outputs at one address are refused.
  */
 typedef struct zero_block_norm_args {
     int64_t rows;          /* 0 <= rows < 2^31 */
@@ -745,7 +745,8 @@ int zero_block_norm(const zero_block_norm_args* args, hipStream_t stream);
  * Absent (data NULL): dh (no norm before the next block; then dx_out is
  * given), dx_out (zeros), dy and what only it needs (no block output: dx
  * alone), and each of dw_pre, dw_post and dgate that is not wanted. dx may be
- * dx_out itself. rows == 0 writes zeros to dw_pre and dw_post.
+ * dx_out itself. Two outputs at one address are refused: where w_pre and w_post
+ * are one vector, its two gradients still need a buffer each. rows == 0 writes zeros to dw_pre and dw_post.
  */
 typedef struct zero_block_norm_grad_args {
     int64_t rows;

@@ -1011,19 +1011,29 @@ def _workspace_of(ws, dev: int):
 
 
 def _stream_of(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream: of device {stream.device_index}, the current device is {dev}")
+    return int(stream.cuda_stream)
+
+
+def _checkpoint(c) -> Act8:
+    if not isinstance(c, Act8):
+        raise TypeError("ckpt: expected an Act8")
+    return c
 
 
 def zero_act8_save(x: torch.Tensor, ckpt: Act8, stream=None) -> None:
     rows, cols, dev = _matrix(x, "x")
-    st = lib().zero_act8_save(_ROWS.pack(*_row_major(x, "x", rows, cols, dev)), rows, cols, int(ckpt.format),
+    st = lib().zero_act8_save(_ROWS.pack(*_row_major(x, "x", rows, cols, dev)), rows, cols, int(_checkpoint(ckpt).format),
                               _act8(ckpt, "ckpt", rows, cols, dev), _stream_of(stream, dev))
     _check(st, "zero_act8_save")
 
 
 def zero_act8_load(ckpt: Act8, out: torch.Tensor, stream=None) -> None:
     rows, cols, dev = _matrix(out, "out")
-    st = lib().zero_act8_load(_act8(ckpt, "ckpt", rows, cols, dev), rows, cols, int(ckpt.format),
+    st = lib().zero_act8_load(_act8(_checkpoint(ckpt), "ckpt", rows, cols, dev), rows, cols, int(ckpt.format),
                               _ROWS.pack(*_row_major(out, "out", rows, cols, dev)), _stream_of(stream, dev))
     _check(st, "zero_act8_load")
 
@@ -1037,7 +1047,7 @@ def zero_act8_wgrad(dy: torch.Tensor, ckpt: Act8, dw: torch.Tensor, flags: int =
     """dw (outs x cols, bf16 or fp32) = dy^T times the checkpoint's rows, its
     columns times col_scale; with GRAD_ACCUMULATE added to an fp32 dw."""
     rows, outs, dev = _matrix(dy, "dy")
-    cols = int(ckpt.cols)
+    cols = int(_checkpoint(ckpt).cols)
     wsp, wsb = _workspace_of(ws, dev)
     scale = None if col_scale is None else _ROWS.pack(*_row_major(col_scale, "col_scale", 1, cols, dev))
     st = lib().zero_act8_wgrad(_ROWS.pack(*_row_major(dy, "dy", rows, outs, dev, torch.bfloat16)),

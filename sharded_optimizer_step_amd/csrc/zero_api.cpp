@@ -2,7 +2,7 @@
 // (fused ZeRO-1, composed, ZeRO-2 streaming, CPU-offloaded, and their
 // dynamic-loss-scale variants): argument checks, host-side scalar
 // derivation, element layouts, the workspace plans and the launch sequences.
-// Every GPU kernel is in zero_kernels.hip; the host optimizer of the
+// Their GPU kernels are in zero_kernels.hip; the host optimizer of the
 // CPU-offloaded step is in zero_host_adamw.cpp.
 #include <hip/hip_runtime.h>
 

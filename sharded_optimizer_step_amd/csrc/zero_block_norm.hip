@@ -11,13 +11,11 @@
 namespace zero {
 namespace {
 
-#ifndef NORM_ROOM
-#define NORM_ROOM 16
-#endif
 // Rows of up to 512 columns take a wave each, four to a workgroup; wider ones
 // a workgroup of as many waves as they have 512 columns.
 constexpr int kWaveVecs = 64;
 constexpr int kMaxLanes = 1024;
+constexpr int kRoomWaves = 16;  // of a compute unit, for rows that stay in registers
 
 // Sums of N values at once over the lanes of a row, in every lane, in a fixed
 // order. The waves of a workgroup meet in LDS: `red` alternates between two
@@ -607,7 +605,7 @@ template <bool WAVE, int V>
 static void norm_shape(NormArgs a, int64_t nv, hipStream_t s)
 {
     const unsigned threads = WAVE ? 256 : block_threads(nv, V);
-    a.unit_rows = rows_a_unit(a.rows, WAVE ? 1 : threads / 64, V == 1 ? NORM_ROOM : 16);
+    a.unit_rows = rows_a_unit(a.rows, WAVE ? 1 : threads / 64, kRoomWaves);
     const int64_t units = (a.rows + a.unit_rows - 1) / a.unit_rows;
     const unsigned grid = static_cast<unsigned>(WAVE ? (units + 3) / 4 : units);
     if (a.x.f32) block_norm_kernel<WAVE, V, true><<<grid, threads, 0, s>>>(a);

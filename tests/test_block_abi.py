@@ -135,7 +135,7 @@ def test_norm_refusals():
     assert norm(rows=0) == OK and norm(cols=0) == OK
 
 
-GRAD = dict(rows=8, cols=64, gate_rows=0, residual_scale=1.0, dx_out=rows(), dx=rows(), dy=rows(), flags=0)
+GRAD = dict(rows=8, cols=64, gate_rows=0, residual_scale=1.0, dx_out=rows(), dx=rows(), dy=rows(data=8192), flags=0)
 GPRE = dict(dh=rows(), w_pre=rows(), rstd_pre=4096, x_out=rows())
 GPOST = dict(w_post=rows(), rstd_post=4096, y=rows())
 
@@ -179,6 +179,19 @@ def test_grad_workspace_is_two_rows_a_unit(r, c, g):
     units = (n - wide) // (8 * c)
     # never more units than rows (the last gate row counted whole), nor many more than the waves that fill the chip
     assert units <= (-(-r // g) * g if g else r) and units <= 2 * 4096
+
+
+def test_two_outputs_at_one_address_are_refused():
+    a, b = rows(data=1 << 20), rows(data=1 << 21)
+    f = dict(PRE, w_post=rows(), x_out=a, h=b, rstd_post=4096, rstd_pre=8192, ckpt_post=4096, ckpt_pre=8192, format=1)
+    for kw in (dict(f, h=a), dict(f, rstd_pre=4096), dict(f, ckpt_pre=4096)):
+        assert norm(**kw) == BAD, kw
+    full = dict(GPRE, **GPOST, gate=rows(), gate_rows=8, dw_pre=rows(data=1 << 16), dw_post=rows(data=1 << 17),
+                dgate=rows(data=1 << 18))
+    small = z.zero_block_norm_grad_workspace_bytes(8, 64, 8) - 1
+    assert grad(wsb=small, **full) == SMALL  # nothing else is wrong with it
+    for kw in (dict(dw_post=full["dw_pre"]), dict(dgate=full["dw_pre"]), dict(dgate=full["dw_post"]), dict(dy=GRAD["dx"])):
+        assert grad(wsb=small, **{**full, **kw}) == BAD, kw
 
 
 def test_packed_structures_are_the_c_ones():
@@ -232,6 +245,15 @@ def test_binding_refuses_host_tensors_and_shapes():
         z._row_major(t[0:1].expand(4, 8), "t", 4, 8, -1)
     with pytest.raises(TypeError):
         z._act8(t, "c", 4, 8, -1)
+    with pytest.raises(TypeError, match="Act8"):
+        z._checkpoint(None)
+
+    class Stream:
+        device_index, cuda_stream = 1, 7
+
+    assert z._stream_of(Stream, 1) == 7
+    with pytest.raises(ValueError, match="stream"):
+        z._stream_of(Stream, 0)
     with pytest.raises(ValueError, match="holds"):
         z._act8(z.Act8(4, 9, 1, t), "c", 4, 8, -1)
     with pytest.raises(ValueError, match="formats"):
