@@ -705,8 +705,10 @@ int zero_act8_wgrad(const zero_rows* dy, const void* ckpt, int64_t rows, int64_t
  * Absent operands (data NULL): y (then x_out is x itself and is not written),
  * w_post (no norm after the block), gate (ones), w_pre (no norm before the
  * next block). rstd_post and rstd_pre (fp32, one per row) are the reciprocal
- * roots; ckpt_post and ckpt_pre the act8 buffers of yn and xn. All sums are
- * fp32; every output is rounded once. Two outputs at one address are refused.
+ * roots; ckpt_post and ckpt_pre the act8 buffers of yn and xn. Sums are held
+ * in fp32 or more and every output is rounded once, the 8-bit codes from the
+ * quotient rather than from its fp32 rounding. Two outputs at one address are
+ * refused.
  */
 typedef struct zero_block_norm_args {
     int64_t rows;          /* 0 <= rows < 2^31 */

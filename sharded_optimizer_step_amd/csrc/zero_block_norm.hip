@@ -62,25 +62,66 @@ __device__ __forceinline__ int64_t row_slot()
     return WAVE ? static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : blockIdx.x;
 }
 
-// 1 / sqrt(sum / cols + eps). The quotient is taken with 1 / cols in two parts
-// and the root refined by one step with an exact residual, which leaves one
-// rounding of each: the 8-bit rows are rounded from what this multiplies, and
-// its error moves some of them to a neighbouring code.
-struct Inverse {
+// The sum of squares of a row: in fp32 over two waves, in fp64 over those.
+template <bool WAVE>
+__device__ __forceinline__ double row_squares(float x, float (*red)[kMaxLanes / 64], int& half)
+{
+    x = wave_sum(x);
+    double s = x;
+    if constexpr (!WAVE) {
+        const int waves = blockDim.x / 64;
+        if (threadIdx.x % 64 == 0) red[half][threadIdx.x / 64] = x;
+        __syncthreads();
+        s = 0.0;
+        for (int w = 0; w < waves; w += 2) s += red[half][w] + (w + 1 < waves ? red[half][w + 1] : 0.0f);
+        half ^= 1;
+    }
+    return s;
+}
+
+// 1 / sqrt(sum / cols + eps) in two parts: an fp32 root corrected by its
+// residual in fp64.
+struct Rstd {
     float hi, lo;
 };
-__device__ __forceinline__ Inverse inverse(int cols)
+__device__ __forceinline__ Rstd row_rstd(double sum, double inv_cols, float eps)
 {
-    const float c = static_cast<float>(cols), hi = 1.0f / c;
-    return Inverse{hi, fmaf(-hi, c, 1.0f) * hi};
+    const double a = fma(sum, inv_cols, static_cast<double>(eps));
+    if (!(a > 0x1p-100 && a < 0x1p100)) return Rstd{1.0f / sqrtf(static_cast<float>(a)), 0.0f};
+    const double r = __builtin_amdgcn_rsqf(static_cast<float>(a));
+    const double root = fma(0.5 * r, fma(-a * r, r, 1.0), r);
+    const float hi = static_cast<float>(root);
+    return Rstd{hi, static_cast<float>(root - hi)};
 }
-__device__ __forceinline__ float row_rstd(float sum, Inverse cols, float eps)
+
+// x / sqrt(..) of 8 columns, as they are rounded to 8 bits with `ties`. A code
+// and the middle of two codes have 8 significant bits at most, so the code of
+// the fp32 product is that of the exact one unless the product ends in 16
+// zeros: those few, one in 65536, go one step towards the exact value.
+__device__ __forceinline__ void normalise(float (&x)[8], Rstd r, bool ties)
 {
-    const float a = fmaf(sum, cols.hi, fmaf(sum, cols.lo, eps));
-    if (!(a > 0x1p-100f && a < 0x1p100f)) return 1.0f / sqrtf(a);
-    const float r = __builtin_amdgcn_rsqf(a), h = a * r;
-    const float off = fmaf(-h, r, 1.0f) - fmaf(a, r, -h) * r;
-    return fmaf(0.5f * r, off, r);
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = x[i] * r.hi;
+    if (ties) {
+        const auto tails = [&](int i) {
+            return __builtin_bit_cast(u16x2, __builtin_amdgcn_perm(__float_as_uint(v[i + 1]), __float_as_uint(v[i]), 0x05040100u));
+        };
+        const u16x2 least = __builtin_elementwise_min(__builtin_elementwise_min(tails(0), tails(2)),
+                                                      __builtin_elementwise_min(tails(4), tails(6)));
+        if (least.x == 0 || least.y == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t bits = __float_as_uint(v[i]);
+                const float off = fmaf(x[i], r.lo, fmaf(x[i], r.hi, -v[i])) * v[i];
+                const uint32_t step = off > 0.0f ? 1u : off < 0.0f ? ~0u : 0u;  // none for a NaN, and for what is exact
+                if ((bits & 0xFFFFu) == 0) v[i] = __uint_as_float(bits + step);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i];
 }
 
 __device__ __forceinline__ void add_squares(float& s, const float (&x)[8])
@@ -113,12 +154,12 @@ template <bool WAVE, int V, bool F32>
 __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(NormArgs a)
 {
     constexpr bool kEarly = V == 1;
-    __shared__ float red[2][1][kMaxLanes / 64];
+    __shared__ float red[2][kMaxLanes / 64];
     int half = 0;
     const int lane = row_lane<WAVE>(), lanes = row_lanes<WAVE>();
     const int nv = static_cast<int>(act8_pitch(a.cols) / 8);
     const int64_t pitch = 8 * static_cast<int64_t>(nv);
-    const Inverse inv_cols = inverse(a.cols);
+    const double inv_cols = 1.0 / a.cols;
     const bool has_y = a.y.p != nullptr, has_post = a.w_post.p != nullptr, has_pre = a.w_pre.p != nullptr;
     int64_t row = row_slot<WAVE>() * a.unit_rows;
     const int64_t end = min(a.rows, row + a.unit_rows);
@@ -153,22 +194,20 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(Norm
         }
         if (kEarly && row + 1 < end) load(row + 1);
         if (has_y) {
-            float rstd = 1.0f;
+            Rstd rstd{1.0f, 0.0f};
             if (has_post) {
-                float s[1] = {0.0f};
+                float s = 0.0f;
 #pragma unroll
-                for (int j = 0; j < V; ++j) add_squares(s[0], y[j]);
-                row_sum<WAVE, 1>(s, red, half);
-                rstd = row_rstd(s[0], inv_cols, a.eps);
-                if (a.rstd_post != nullptr && lane == 0) ((ZERO_G float*)a.rstd_post)[row] = rstd;
+                for (int j = 0; j < V; ++j) add_squares(s, y[j]);
+                rstd = row_rstd(row_squares<WAVE>(s, red, half), inv_cols, a.eps);
+                if (a.rstd_post != nullptr && lane == 0) ((ZERO_G float*)a.rstd_post)[row] = rstd.hi;
             }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int v = lane + j * lanes, n = a.cols - 8 * v;
                 if (v >= nv) continue;
                 if (!kEarly) load_gain(a.gate, a.w_post, a.alpha, g, v, n, e);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[j][i] *= rstd;
+                if (has_post) normalise(y[j], rstd, a.ckpt_post != nullptr);
                 if (a.ckpt_post != nullptr) save8(a.ckpt_post, a.rows, pitch, a.format, row, v, y[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[j][i] = fmaf(e[i], y[j][i], x[j][i]);
@@ -178,19 +217,17 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(Norm
             }
         }
         if (has_pre) {
-            float s[1] = {0.0f};
+            float s = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) add_squares(s[0], x[j]);
-            row_sum<WAVE, 1>(s, red, half);
-            const float rstd = row_rstd(s[0], inv_cols, a.eps);
-            if (a.rstd_pre != nullptr && lane == 0) ((ZERO_G float*)a.rstd_pre)[row] = rstd;
+            for (int j = 0; j < V; ++j) add_squares(s, x[j]);
+            const Rstd rstd = row_rstd(row_squares<WAVE>(s, red, half), inv_cols, a.eps);
+            if (a.rstd_pre != nullptr && lane == 0) ((ZERO_G float*)a.rstd_pre)[row] = rstd.hi;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int v = lane + j * lanes, n = a.cols - 8 * v;
                 if (v >= nv) continue;
                 if (!kEarly) load8_any(a.w_pre, 0, 8 * v, n, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] *= rstd;
+                normalise(x[j], rstd, a.ckpt_pre != nullptr);
                 if (a.ckpt_pre != nullptr) save8(a.ckpt_pre, a.rows, pitch, a.format, row, v, x[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[j][i] = x[j][i] * w[i];

@@ -113,6 +113,51 @@ def test_forward_operands(y, post, pre, gate_rows, saves):
         assert canary_ok(buf, rows, cols, 3, 1)
 
 
+def integers_of_mean_square(g, count, mean, low, most):
+    """count whole numbers, most of them in 0 .. low and none above `most`, whose squares sum to count * mean."""
+    squares = {a * a + b * b: (a, b) for a in range(most + 1) for b in range(a + 1)}
+    while True:
+        n = [int(v) for v in torch.randint(0, low + 1, (count - 4,), generator=g)]
+        rest = count * mean - sum(v * v for v in n)
+        for half, (a, b) in squares.items():
+            if rest - half in squares:
+                n += [a, b, *squares[rest - half]]
+                return torch.tensor(n)[torch.randperm(count, generator=g)]
+
+
+@pytest.mark.parametrize("cols", [64, 800])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_forward_rounds_the_exact_quotient(fmt, cols):
+    # The squares' mean is exactly 1 (and their sums whole numbers below 2^24 of one unit) and eps 2^-24, so the exact factor is 1 - 2^-25, whose nearest fp32 number is 1:
+    # the fp32 products are the values themselves, many of them the middle of two codes, and the exact ones a hair
+    # below, so each of those goes to the code nearer to zero. e4m3 codes have 4 bits: sixteenths from 16 to 31 have one
+    # too many; int8 codes of blocks with a value over 127/128 are multiples of 1/64, the values of 1/128.
+    g = torch.Generator().manual_seed(cols)
+    unit, low, most = (16, 27, 31) if fmt == "e4m3" else (128, 221, 254)
+    n = torch.stack([integers_of_mean_square(g, cols, unit * unit, low, most) for _ in range(5)])
+    if fmt == "int8":
+        assert bool((n.reshape(5, -1, 32).amax(2) > 127).all())
+    sign = torch.where(torch.rand(n.shape, generator=g) < 0.5, -1, 1)
+    down = torch.where(n > 16, n - n % 2, n) if fmt == "e4m3" else n - n % 2
+    assert int((down != n).sum()) > n.numel() // 8
+    want = (sign * down).double() / unit
+    v = ((sign * n).double() / unit).to("cuda")
+    one, out, h = (torch.ones(cols, device="cuda"), torch.empty(5, cols, device="cuda"),
+                   torch.empty(5, cols, dtype=torch.bfloat16, device="cuda"))
+    for where in ("pre", "post"):
+        ck, rstd = z.new_act8(5, cols, FORMATS[fmt]), torch.empty(5, device="cuda")
+        if where == "pre":
+            b = z.BlockNorm(x=v.float(), w_pre=one, h=h, rstd_pre=rstd, ckpt_pre=ck, eps=2.0**-24)
+        else:
+            b = z.BlockNorm(x=torch.zeros(5, cols, device="cuda"), y=v.bfloat16(), w_post=one, x_out=out, rstd_post=rstd,
+                            ckpt_post=ck, eps=2.0**-24)
+        z.zero_block_norm(b)
+        got = torch.empty(5, cols, device="cuda")
+        z.zero_act8_load(ck, got)
+        assert torch.equal(rstd.cpu(), torch.ones(5)), where
+        assert torch.equal(got.double().cpu(), want), where
+
+
 def test_forward_in_place_and_nonfinite_rows():
     b, _ = forward(8, 200, resid=torch.float32)
     x = b.x.clone()
