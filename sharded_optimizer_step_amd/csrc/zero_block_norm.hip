@@ -684,9 +684,17 @@ NormGradPlan norm_grad_plan(int64_t rows, int64_t cols, int64_t gate_rows)
         p.unit_gates = (p.gates + target - 1) / target;
         p.units = (p.gates + p.unit_gates - 1) / p.unit_gates;
     } else if (p.gates > 0) {
-        p.per_gate = target / p.gates;
-        if (p.per_gate > p.gate_rows) p.per_gate = p.gate_rows;
-        p.unit_rows = (p.gate_rows + p.per_gate - 1) / p.per_gate;
+        // the fewest rows a unit with which the units that have rows run at
+        // once (more rows a unit never make more units)
+        const int64_t last = rows - (p.gates - 1) * p.gate_rows;
+        int64_t least = (rows + target - 1) / target, most = p.gate_rows;
+        while (least < most) {
+            const int64_t r = least + (most - least) / 2;
+            const int64_t units = (p.gates - 1) * ((p.gate_rows + r - 1) / r) + (last + r - 1) / r;
+            if (units <= target) most = r;
+            else least = r + 1;
+        }
+        p.unit_rows = most;
         p.per_gate = (p.gate_rows + p.unit_rows - 1) / p.unit_rows;
         // the last gate row may be short: its units past the end sum nothing
         p.units = p.gates * p.per_gate;
