@@ -78,7 +78,7 @@ __global__ __launch_bounds__(kActThreads) void act8_load_kernel(const uint8_t* c
         if (first + i >= total) continue;
         float f[8];
         decode8<FMT>(c[u], s[u], f);
-        store8<F32>(out, at[u].row, 8 * at[u].v, cols - 8 * at[u].v, f);
+        store8<F32, true>(out, at[u].row, 8 * at[u].v, cols - 8 * at[u].v, f);
     }
 }
 

@@ -23,10 +23,28 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 
-__device__ __forceinline__ u32x4 ld16_a2(const void* p) { return *(const ZERO_G u32x4_a2*)p; }
-__device__ __forceinline__ u32x4 ld16_a4(const void* p) { return *(const ZERO_G u32x4_a4*)p; }
-__device__ __forceinline__ void st16_a2(void* p, u32x4 v) { *(ZERO_G u32x4_a2*)p = v; }
-__device__ __forceinline__ void st16_a4(void* p, u32x4 v) { *(ZERO_G u32x4_a4*)p = v; }
+// STREAM: a line that this kernel does not touch again should not displace
+// others from the caches.
+template <bool STREAM, class T>
+__device__ __forceinline__ u32x4 ld16_as(const void* p)
+{
+    if constexpr (STREAM) return __builtin_nontemporal_load((const ZERO_G T*)p);
+    else return *(const ZERO_G T*)p;
+}
+template <bool STREAM, class T>
+__device__ __forceinline__ void st16_as(void* p, u32x4 v)
+{
+    if constexpr (STREAM) __builtin_nontemporal_store(v, (ZERO_G T*)p);
+    else *(ZERO_G T*)p = v;
+}
+template <bool STREAM = false>
+__device__ __forceinline__ u32x4 ld16_a2(const void* p) { return ld16_as<STREAM, u32x4_a2>(p); }
+template <bool STREAM = false>
+__device__ __forceinline__ u32x4 ld16_a4(const void* p) { return ld16_as<STREAM, u32x4_a4>(p); }
+template <bool STREAM = false>
+__device__ __forceinline__ void st16_a2(void* p, u32x4 v) { st16_as<STREAM, u32x4_a2>(p, v); }
+template <bool STREAM = false>
+__device__ __forceinline__ void st16_a4(void* p, u32x4 v) { st16_as<STREAM, u32x4_a4>(p, v); }
 
 // Eight values as loaded: bf16 in one 16-byte load, fp32 in two.
 template <bool F32>
@@ -50,17 +68,17 @@ __device__ __forceinline__ int back(int col, int n) { return n > 0 && n < 8 && c
 
 // Eight elements of a row from column col, to be unpacked with the same col
 // and n; elements from `n` on are not read.
-template <bool F32>
+template <bool F32, bool STREAM = false>
 __device__ __forceinline__ Raw8<F32> load8(const Rows& m, int64_t row, int col, int n)
 {
     Raw8<F32> r{};
     const char* p = row_at<F32>(m, row, col - back(col, n));
     if (n >= 8 || (n > 0 && col > 0)) {
         if constexpr (F32) {
-            r.v[0] = ld16_a4(p);
-            r.v[1] = ld16_a4(p + 16);
+            r.v[0] = ld16_a4<STREAM>(p);
+            r.v[1] = ld16_a4<STREAM>(p + 16);
         } else {
-            r.v[0] = ld16_a2(p);
+            r.v[0] = ld16_a2<STREAM>(p);
         }
     } else if (n > 0) {  // the row has fewer than 8 columns
 #pragma unroll
@@ -117,14 +135,14 @@ __device__ __forceinline__ void round_bf16(float (&f)[8])
 }
 
 // The first n of eight values to p, rounded to bf16 or as they are.
-template <bool F32>
+template <bool F32, bool STREAM = false>
 __device__ __forceinline__ void store8(const Rows& m, int64_t row, int col, int n, const float (&f)[8])
 {
     if constexpr (F32) {
         char* p = row_at<true>(m, row, col);
         if (n >= 8) {
-            st16_a4(p, __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]}));
-            st16_a4(p + 16, __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]}));
+            st16_a4<STREAM>(p, __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]}));
+            st16_a4<STREAM>(p + 16, __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]}));
         } else {
 #pragma unroll
             for (int i = 0; i < 7; ++i)
@@ -134,7 +152,7 @@ __device__ __forceinline__ void store8(const Rows& m, int64_t row, int col, int 
         char* p = row_at<false>(m, row, col);
         const u32x4 v = pack8(f);
         if (n >= 8) {
-            st16_a2(p, v);
+            st16_a2<STREAM>(p, v);
         } else {
 #pragma unroll
             for (int i = 0; i < 7; ++i)

@@ -38,6 +38,12 @@ struct Rows {
     int32_t f32;  // fp32, else bf16
 };
 
+// Every row of m starts on 16 bytes (so does an absent operand's).
+inline bool rows_on_16(const Rows& m)
+{
+    return (reinterpret_cast<uintptr_t>(m.p) | static_cast<uint64_t>(m.ld) * (m.f32 ? 4 : 2)) % 16 == 0;
+}
+
 hipError_t launch_act8_save(const Rows& x, int64_t rows, int64_t cols, int format, uint8_t* ckpt, hipStream_t s);
 hipError_t launch_act8_load(const uint8_t* ckpt, int64_t rows, int64_t cols, int format, const Rows& out,
                             hipStream_t s);
@@ -74,6 +80,7 @@ struct NormArgs {
     int64_t unit_rows;  // rows that a workgroup (or wave) takes, set at the launch
     int32_t cols;
     float alpha, eps;
+    int32_t stream;  // read x and y past the caches, set at the launch
     Rows x, y, w_post, gate, w_pre, x_out, h;
     FastDiv gate_div;
     float* rstd_post;
@@ -111,6 +118,7 @@ struct NormGradArgs {
     const float* rstd_post;
     int format;
     int accumulate;
+    int stream;  // write dx and dy past the caches, set at the launch
     NormGradPlan plan;
     FastDiv gate_div;
     float* sum_pre;   // [units][cols]: sums of dh * xn

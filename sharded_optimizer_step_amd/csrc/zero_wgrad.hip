@@ -91,7 +91,7 @@ __device__ __forceinline__ void store_dw(const WgradArgs& a, int64_t m, int64_t 
         uint16_t* p = static_cast<uint16_t*>(a.dw.p) + m * a.dw.ld + n;
         const u32x2 w{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
         typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-        if (left == 4) *(ZERO_G u32x2_a2*)p = w;
+        if (left == 4) __builtin_nontemporal_store(w, (ZERO_G u32x2_a2*)p);
         else {
 #pragma unroll
             for (int r = 0; r < 3; ++r)

@@ -406,6 +406,35 @@ def test_captured_and_replayed(cols):
             assert torch.equal(getattr(d, n), replayed[n]), (n, i)
 
 
+@pytest.mark.parametrize("resid,rows,cols", [(torch.bfloat16, 9000, 4096), (torch.float32, 6000, 4104), (torch.bfloat16, 1800, 16384)])
+def test_large_calls_give_what_small_ones_do(resid, rows, cols):
+    # a call that moves more than the caches hold reads and writes past them; its rows are independent of each other
+    g = gen(11)
+    x, y = rnd(g, rows, cols, dtype=resid), rnd(g, rows, cols, dtype=torch.bfloat16)
+    w_post, w_pre = rnd(g, cols, dtype=torch.bfloat16), rnd(g, cols, dtype=torch.bfloat16)
+
+    def go(lo, hi, in_place=False):
+        n = hi - lo
+        ck = [z.new_act8(n, cols), z.new_act8(n, cols)]
+        src = x[lo:hi].clone() if in_place else x[lo:hi]
+        out = src if in_place else torch.empty_like(src)
+        h = torch.empty(n, cols, dtype=torch.bfloat16, device="cuda")
+        z.zero_block_norm(z.BlockNorm(x=src, y=y[lo:hi], w_post=w_post, w_pre=w_pre, x_out=out, h=h, ckpt_post=ck[0],
+                                      ckpt_pre=ck[1], residual_scale=0.7))
+        back = torch.empty(n, cols, dtype=torch.bfloat16, device="cuda")
+        z.zero_act8_load(ck[1], back)
+        return out, h, back
+
+    assert rows * cols * (2 * x.element_size() + 6) > 256 << 20
+    whole = go(0, rows)
+    for a, b in zip(whole, go(0, rows, in_place=True)):
+        assert torch.equal(a, b)
+    step = rows // 5 + 1
+    for lo in range(0, rows, step):
+        for a, b in zip(whole, go(lo, min(rows, lo + step))):
+            assert torch.equal(a[lo:lo + step], b)
+
+
 def test_offsets_past_32_bits():
     rows, cols, ld = 70, 300, 1 << 25
     big = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda")
