@@ -3,7 +3,10 @@
 // Both are streams: 8 columns (one 16-byte bf16 load) a thread, four threads
 // to a block of 32 columns, whose largest value they find with two quad
 // permutes. The rows are visited as one list of 8-column vectors, so narrow
-// and odd rows fill a wave like wide ones.
+// and odd rows fill a wave like wide ones. HBM bounds both: 16384 x 4096 bf16
+// (3.03 bytes a value) is saved in 40 us and read back in 30, 5.1 and 6.8 TB/s
+// (part of it from the Infinity Cache), where a copy of 2 GiB runs at 4.9; a
+// call of 129 x 771 takes 4.5 us, a launch's latency.
 #include "zero_act8_device.h"
 
 namespace zero {
