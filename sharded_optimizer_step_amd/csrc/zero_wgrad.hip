@@ -8,14 +8,15 @@
 // from memory to LDS: a power-of-two scale makes that exact, so the product
 // is the bf16 one, with half the reads of X.
 //
-// Large products are bound by their matrix instructions and by the LDS reads
-// that feed them, which take as long (256 x 256 tiles: 1024 clocks each for 32
-// tokens), at the 2.0 to 2.1 GHz that the chip holds under this load. 8192
-// tokens: 11008 x 4096 from e4m3 to bf16 648 us (1.14 PFLOP/s; 2.7 rounds of
-// tiles), 4096 x 4096 from int8 added to fp32 271 us (1.01; the last 35 us read
-// and write dW), to bf16 212 us (1.30). The matrix units are busy 55% of the
-// cycles, LDS has conflicts in 0.6%. Small ones are bound by a tile's start and
-// the latency of its steps: 192 tokens and 768 x 768 5.6 us.
+// Large products are bound by their matrix instructions (busy 56% of the
+// cycles, LDS 36% with conflicts in 0.6%) and by what does not overlap with
+// them: a wave decodes and stages a tile, then multiplies one, and the two
+// waves of a SIMD do so nearly together; at the 2.0 to 2.1 GHz that the chip
+// holds under this load. 8192 tokens: 11008 x 4096 from e4m3 to bf16 648 us
+// (1.14 PFLOP/s; 2.7 rounds of tiles), 4096 x 4096 from int8 added to fp32 271
+// us (1.01; 27 of them the 134 MB of dW read and written at the rate of a
+// copy). Small ones are bound by a tile's start and the latency of its steps:
+// 192 tokens and 768 x 768 5.6 us.
 #include "zero_act8_device.h"
 
 namespace zero {
