@@ -954,6 +954,8 @@ def _row_major(t, name: str, rows: int, cols: int, dev: int, only=None):
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         _on(t, name, dev)
     dtype = t.dtype
+    if t.shape == (rows, cols) and t.is_contiguous() and (dtype is only if only is not None else dtype in _DTYPES):
+        return t.data_ptr(), cols, _DTYPES[dtype], 0  # most operands, in fewer steps than the checks below
     if dtype not in _DTYPES or (only is not None and dtype is not only):
         raise TypeError(f"{name}: expected {only or 'torch.bfloat16 or torch.float32'}, got {dtype}")
     dim = t.dim()
@@ -975,12 +977,23 @@ def _row_major(t, name: str, rows: int, cols: int, dev: int, only=None):
     return t.data_ptr(), ld, _DTYPES[dtype], 0
 
 
+def _vector(t, name: str, cols: int, dev: int):
+    """A row of cols elements, as one dimension or a matrix of one row."""
+    if t is None:
+        return _ABSENT
+    if isinstance(t, torch.Tensor) and t.shape == (cols,) and t.get_device() == dev and t.is_contiguous():
+        dtype = t.dtype
+        if dtype in _DTYPES:
+            return t.data_ptr(), cols, _DTYPES[dtype], 0
+    return _row_major(t, name, 1, cols, dev)
+
+
 def _per_row(t, name: str, rows: int, dev: int) -> int:
     if t is None:
         return 0
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         _on(t, name, dev)
-    if t.dtype is not torch.float32 or t.numel() != rows or not t.is_contiguous():
+    if t.shape != (rows,) or t.dtype is not torch.float32 or not t.is_contiguous():
         _need(t, torch.float32, name, rows)
     return t.data_ptr()
 
@@ -1049,7 +1062,7 @@ def zero_act8_wgrad(dy: torch.Tensor, ckpt: Act8, dw: torch.Tensor, flags: int =
     rows, outs, dev = _matrix(dy, "dy")
     cols = int(_checkpoint(ckpt).cols)
     wsp, wsb = _workspace_of(ws, dev)
-    scale = None if col_scale is None else _ROWS.pack(*_row_major(col_scale, "col_scale", 1, cols, dev))
+    scale = None if col_scale is None else _ROWS.pack(*_vector(col_scale, "col_scale", cols, dev))
     st = lib().zero_act8_wgrad(_ROWS.pack(*_row_major(dy, "dy", rows, outs, dev, torch.bfloat16)),
                                _act8(ckpt, "ckpt", rows, cols, dev), rows, outs, cols, int(ckpt.format), scale,
                                _ROWS.pack(*_row_major(dw, "dw", outs, cols, dev)), int(flags), wsp, wsb,
@@ -1122,8 +1135,8 @@ def zero_block_norm(b: BlockNorm, stream=None) -> None:
     gate = _ABSENT if b.gate is None else _row_major(b.gate, "gate", _gates(rows, b.gate_rows), cols, dev)
     args = _BLOCK_NORM.pack(
         rows, cols, b.gate_rows, b.residual_scale, b.eps, *_row_major(b.x, "x", rows, cols, dev),
-        *_row_major(b.y, "y", rows, cols, dev, bf16), *_row_major(b.w_post, "w_post", 1, cols, dev), *gate,
-        *_row_major(b.w_pre, "w_pre", 1, cols, dev), *_row_major(b.x_out, "x_out", rows, cols, dev, b.x.dtype),
+        *_row_major(b.y, "y", rows, cols, dev, bf16), *_vector(b.w_post, "w_post", cols, dev), *gate,
+        *_vector(b.w_pre, "w_pre", cols, dev), *_row_major(b.x_out, "x_out", rows, cols, dev, b.x.dtype),
         *_row_major(b.h, "h", rows, cols, dev, bf16), _per_row(b.rstd_post, "rstd_post", rows, dev),
         _per_row(b.rstd_pre, "rstd_pre", rows, dev), _act8(b.ckpt_post, "ckpt_post", rows, cols, dev),
         _act8(b.ckpt_pre, "ckpt_pre", rows, cols, dev), _act8_format(b.ckpt_post, b.ckpt_pre), 0)
@@ -1142,13 +1155,13 @@ def zero_block_norm_grad(b: BlockNormGrad, flags: int = 0, ws: Optional[torch.Te
     wsp, wsb = _workspace_of(ws, dev)
     args = _BLOCK_NORM_GRAD.pack(
         rows, cols, b.gate_rows, b.residual_scale, *_row_major(b.dh, "dh", rows, cols, dev, bf16),
-        *_row_major(b.dx_out, "dx_out", rows, cols, dev, like), *_row_major(b.w_post, "w_post", 1, cols, dev),
-        *_row_major(b.gate, "gate", gates, cols, dev), *_row_major(b.w_pre, "w_pre", 1, cols, dev),
+        *_row_major(b.dx_out, "dx_out", rows, cols, dev, like), *_vector(b.w_post, "w_post", cols, dev),
+        *_row_major(b.gate, "gate", gates, cols, dev), *_vector(b.w_pre, "w_pre", cols, dev),
         *_row_major(b.x_out, "x_out", rows, cols, dev, like), *_row_major(b.y, "y", rows, cols, dev, bf16),
         _act8(b.ckpt_pre, "ckpt_pre", rows, cols, dev), _act8(b.ckpt_post, "ckpt_post", rows, cols, dev),
         _per_row(b.rstd_pre, "rstd_pre", rows, dev), _per_row(b.rstd_post, "rstd_post", rows, dev),
         *_row_major(b.dx, "dx", rows, cols, dev), *_row_major(b.dy, "dy", rows, cols, dev, bf16),
-        *_row_major(b.dw_pre, "dw_pre", 1, cols, dev), *_row_major(b.dw_post, "dw_post", 1, cols, dev),
+        *_vector(b.dw_pre, "dw_pre", cols, dev), *_vector(b.dw_post, "dw_post", cols, dev),
         *_row_major(b.dgate, "dgate", gates, cols, dev), _act8_format(b.ckpt_post, b.ckpt_pre), flags)
     _check(lib().zero_block_norm_grad(args, wsp, wsb, _stream_of(stream, dev)), "zero_block_norm_grad")
 
