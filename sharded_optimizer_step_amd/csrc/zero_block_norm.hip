@@ -100,30 +100,29 @@ __device__ __forceinline__ Rstd row_rstd(double sum, double inv_cols, float eps)
     return Rstd{hi, static_cast<float>(root - hi)};
 }
 
-// x / sqrt(..) of 8 columns, as they are rounded to 8 bits with `ties`. A code
-// and the middle of two codes have 8 significant bits at most, so the code of
-// the fp32 product is that of the exact one unless the product ends in 16
-// zeros: those few, one in 65536, go one step towards the exact value.
-__device__ __forceinline__ void normalise(float (&x)[8], Rstd r, bool ties)
+// x / sqrt(..) of 8 columns. A code and the middle of two codes have 8
+// significant bits at most, so the code of the fp32 product is that of the
+// exact one unless the product ends in 16 zeros: those few, one in 65536, go
+// one step towards the exact value. (Also where no checkpoint is written: what
+// a call computes does not depend on what it saves.)
+__device__ __forceinline__ void normalise(float (&x)[8], Rstd r)
 {
     typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = x[i] * r.hi;
-    if (ties) {
-        const auto tails = [&](int i) {
-            return __builtin_bit_cast(u16x2, __builtin_amdgcn_perm(__float_as_uint(v[i + 1]), __float_as_uint(v[i]), 0x05040100u));
-        };
-        const u16x2 least = __builtin_elementwise_min(__builtin_elementwise_min(tails(0), tails(2)),
-                                                      __builtin_elementwise_min(tails(4), tails(6)));
-        if (least.x == 0 || least.y == 0) {
+    const auto tails = [&](int i) {
+        return __builtin_bit_cast(u16x2, __builtin_amdgcn_perm(__float_as_uint(v[i + 1]), __float_as_uint(v[i]), 0x05040100u));
+    };
+    const u16x2 least = __builtin_elementwise_min(__builtin_elementwise_min(tails(0), tails(2)),
+                                                  __builtin_elementwise_min(tails(4), tails(6)));
+    if (least.x == 0 || least.y == 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t bits = __float_as_uint(v[i]);
-                const float off = fmaf(x[i], r.lo, fmaf(x[i], r.hi, -v[i])) * v[i];
-                const uint32_t step = off > 0.0f ? 1u : off < 0.0f ? ~0u : 0u;  // none for a NaN, and for what is exact
-                if ((bits & 0xFFFFu) == 0) v[i] = __uint_as_float(bits + step);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t bits = __float_as_uint(v[i]);
+            const float off = fmaf(x[i], r.lo, fmaf(x[i], r.hi, -v[i])) * v[i];
+            const uint32_t step = off > 0.0f ? 1u : off < 0.0f ? ~0u : 0u;  // none for a NaN, and for what is exact
+            if ((bits & 0xFFFFu) == 0) v[i] = __uint_as_float(bits + step);
         }
     }
 #pragma unroll
@@ -220,7 +219,7 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(Norm
                 const int v = lane + j * lanes, n = a.cols - 8 * v;
                 if (v >= nv) continue;
                 if (!kEarly) load_gain(a.gate, a.w_post, a.alpha, g, v, n, e);
-                if (has_post) normalise(y[j], rstd, a.ckpt_post != nullptr);
+                if (has_post) normalise(y[j], rstd);
                 if (a.ckpt_post != nullptr) save8(a.ckpt_post, a.rows, pitch, a.format, row, v, y[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[j][i] = fmaf(e[i], y[j][i], x[j][i]);
@@ -240,7 +239,7 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void block_norm_kernel(Norm
                 const int v = lane + j * lanes, n = a.cols - 8 * v;
                 if (v >= nv) continue;
                 if (!kEarly) load8_any(a.w_pre, 0, 8 * v, n, w);
-                normalise(x[j], rstd, a.ckpt_pre != nullptr);
+                normalise(x[j], rstd);
                 if (a.ckpt_pre != nullptr) save8(a.ckpt_pre, a.rows, pitch, a.format, row, v, x[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[j][i] = x[j][i] * w[i];

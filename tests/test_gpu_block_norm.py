@@ -158,6 +158,14 @@ def test_forward_rounds_the_exact_quotient(fmt, cols):
         assert torch.equal(got.double().cpu(), want), where
 
 
+def test_forward_does_not_depend_on_what_it_saves():
+    b, _ = forward(300, 1000, gate_rows=100)
+    z.zero_block_norm(b)
+    keep = [t.clone() for t in (b.x_out, b.h)]
+    z.zero_block_norm(dataclasses.replace(b, ckpt_post=None, ckpt_pre=None, rstd_post=None, rstd_pre=None))
+    assert torch.equal(keep[0], b.x_out) and torch.equal(keep[1], b.h)
+
+
 def test_forward_in_place_and_nonfinite_rows():
     b, _ = forward(8, 200, resid=torch.float32)
     x = b.x.clone()
