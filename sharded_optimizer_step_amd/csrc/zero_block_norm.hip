@@ -685,6 +685,8 @@ hipError_t launch_block_norm(const NormArgs& args, hipStream_t s)
     NormArgs a = args;
     a.stream = streams_inputs(a);
     const int64_t nv = act8_pitch(a.cols) / 8;
+    // one vector a lane as long as a workgroup has the lanes: 8192 x 8192 with
+    // both reads 213 us, 231 with two; 3001 x 5003 81 and 102
     if (nv <= kWaveVecs) norm_shape<true, 1>(a, nv, s);
     else if (nv <= kMaxLanes) norm_shape<false, 1>(a, nv, s);
     else norm_shape<false, 2>(a, nv, s);
