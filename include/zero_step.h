@@ -688,7 +688,8 @@ size_t zero_act8_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols)
  * 2^30, and dw has fewer than 2^20 tiles of 128 x 128 (1.7e10 elements).
  * ws: device workspace of zero_act8_wgrad_workspace_bytes(...) bytes, 16-byte
  * aligned (NULL if that is 0), contents irrelevant on entry and not kept; two
- * calls that share one must not run concurrently.
+ * calls that share one must not run concurrently. The plan that a step keeps in
+ * any part of it is forgotten, as by zero_workspace_forget.
  */
 int zero_act8_wgrad(const zero_rows* dy, const void* ckpt, int64_t rows, int64_t outs, int64_t cols, int32_t format,
                     const zero_rows* col_scale, const zero_rows* dw, int32_t flags, void* ws, size_t ws_bytes,
@@ -781,7 +782,8 @@ size_t zero_block_norm_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t 
 
 /* ws: device workspace of that size, 16-byte aligned (NULL if it is 0),
  * contents irrelevant on entry and not kept; two calls that share one must not
- * run concurrently. */
+ * run concurrently. The plan that a step keeps in any part of it is forgotten,
+ * as by zero_workspace_forget. */
 int zero_block_norm_grad(const zero_block_norm_grad_args* args, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*

@@ -192,17 +192,12 @@ uint64_t fnv1a(const uint8_t* p, size_t n, uint64_t h)
     return h;
 }
 
+struct HeldPlan {
+    uint64_t sig;
+    size_t bytes;  // of the workspace, from its start
+};
 std::mutex g_plan_mu;
-std::map<std::pair<int, uintptr_t>, uint64_t> g_plan_cache;  // (device, ws) -> signature held there
-
-void forget_ws(const void* ws)
-{
-    std::lock_guard<std::mutex> lk(g_plan_mu);
-    for (auto it = g_plan_cache.begin(); it != g_plan_cache.end();) {
-        if (it->first.second == reinterpret_cast<uintptr_t>(ws)) it = g_plan_cache.erase(it);
-        else ++it;
-    }
-}
+std::map<std::pair<int, uintptr_t>, HeldPlan> g_plan_cache;  // (device, ws) -> the plan held there
 
 // One tensor of a plan: the M replica pointers of the passes that fold them,
 // the state and output of the passes that update, and the caller's fp32
@@ -336,7 +331,7 @@ int make_plan(const std::vector<PlanTensor>& ts, int32_t M, PlanKind kind, void*
     {
         std::lock_guard<std::mutex> lk(g_plan_mu);
         auto it = g_plan_cache.find(key);
-        cached = it != g_plan_cache.end() && it->second == sig;
+        cached = it != g_plan_cache.end() && it->second.sig == sig;
     }
     plan->gbuf.assign(static_cast<size_t>(T), nullptr);
     plan->layouts = layouts;
@@ -378,7 +373,7 @@ int make_plan(const std::vector<PlanTensor>& ts, int32_t M, PlanKind kind, void*
         std::memcpy(c.data, blob.data(), off.desc);
         if (launch_plan_write(wsb, c, stream) != hipSuccess) return ZERO_ERR_HIP;
         std::lock_guard<std::mutex> lk(g_plan_mu);
-        g_plan_cache[key] = sig;
+        g_plan_cache[key] = HeldPlan{sig, off.total};
     }
     return ZERO_OK;
 }
@@ -469,6 +464,21 @@ int step_impl(const zero_tensor* tensors, int32_t T, int32_t M, const zero_adamw
 
 }  // namespace
 
+namespace zero {
+
+void forget_plans(const void* ws, size_t bytes)
+{
+    const uintptr_t from = reinterpret_cast<uintptr_t>(ws);
+    std::lock_guard<std::mutex> lk(g_plan_mu);
+    for (auto it = g_plan_cache.begin(); it != g_plan_cache.end();) {
+        const uintptr_t at = it->first.second;
+        if (at < from + bytes && from < at + it->second.bytes) it = g_plan_cache.erase(it);
+        else ++it;
+    }
+}
+
+}  // namespace zero
+
 extern "C" {
 
 const char* zero_status_string(int status)
@@ -531,7 +541,7 @@ int zero_grad_check_norm(const float* g, int64_t n, const zero_adamw_hparams* hp
     if (g == nullptr || ws == nullptr) return ZERO_ERR_INVALID_ARGUMENT;
     if (reinterpret_cast<uintptr_t>(ws) % 16u != 0) return ZERO_ERR_INVALID_ARGUMENT;
     if (ws_bytes < zero_grad_check_norm_workspace_bytes(n)) return ZERO_ERR_WORKSPACE_TOO_SMALL;
-    forget_ws(ws);  // a zero_step plan cached in this workspace is overwritten
+    forget_plans(ws, zero_grad_check_norm_workspace_bytes(n));  // a zero_step plan cached there is overwritten
     const Layout L = make_layout(n, {}, {reinterpret_cast<uintptr_t>(g)});
     const int grid = grid_for(layout_tiles(L), resident_grid_check());
     Partial* parts = static_cast<Partial*>(ws);
@@ -1297,7 +1307,7 @@ int zero_offload_step_amp(const zero_offload_tensor* tensors, int32_t T, int32_t
 int zero_workspace_forget(const void* ws)
 {
     if (ws == nullptr) return ZERO_ERR_INVALID_ARGUMENT;
-    forget_ws(ws);
+    forget_plans(ws, 1);
     return ZERO_OK;
 }
 

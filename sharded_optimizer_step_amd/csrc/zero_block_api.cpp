@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "zero_block.h"
+#include "zero_internal.h"
 #include "zero_step.h"
 
 using namespace zero;
@@ -119,6 +120,7 @@ int zero_act8_wgrad(const zero_rows* dy, const void* ckpt, int64_t rows, int64_t
     if (plan.bytes > 0) {
         if (!buffer_ok(ws)) return ZERO_ERR_INVALID_ARGUMENT;
         if (ws_bytes < plan.bytes) return ZERO_ERR_WORKSPACE_TOO_SMALL;
+        forget_plans(ws, plan.bytes);
     }
     a.dy = static_cast<const uint16_t*>(dy->data);
     a.ld_dy = dy->ld;
@@ -235,6 +237,7 @@ int zero_block_norm_grad(const zero_block_norm_grad_args* g, void* ws, size_t ws
     if (a.plan.bytes > 0) {
         if (!buffer_ok(ws)) return ZERO_ERR_INVALID_ARGUMENT;
         if (ws_bytes < a.plan.bytes) return ZERO_ERR_WORKSPACE_TOO_SMALL;
+        forget_plans(ws, a.plan.bytes);
     }
     a.dh = view(g->dh);
     a.dx_out = view(g->dx_out);

@@ -175,6 +175,10 @@ enum class Mode : int {
                      // emit, norm partials into the bucket partial (no clipping, no skipping)
 };
 
+// Drops the host-side records of plans in any part of [ws, ws + bytes): a call
+// that is about to overwrite it (zero_api.cpp).
+void forget_plans(const void* ws, size_t bytes);
+
 // ---- launch wrappers (zero_kernels.hip); all return a hipError_t ----------
 
 hipError_t launch_reduce(const RankPtrs& ptrs, int Mc, bool first, bool last, float scale, const Layout& L,
