@@ -121,8 +121,8 @@ struct NormGradArgs {
     int stream;  // write dx and dy past the caches, set at the launch
     NormGradPlan plan;
     FastDiv gate_div;
-    float* sum_pre;   // [units][cols]: sums of dh * xn
-    float* sum_post;  // [units][cols]: sums of d * yn (few gate rows), or of gate * d * yn (many)
+    float* sum_pre;   // [units][cols]: sums of dh * xn, for dw_pre
+    float* sum_post;  // [units][cols]: sums of d * yn (few gate rows, for dw_post and dgate), or of gate * d * yn (many, for dw_post)
     float* row_sums;  // [rows][2] with strips
 };
 hipError_t launch_block_norm_grad(const NormGradArgs& a, hipStream_t s);

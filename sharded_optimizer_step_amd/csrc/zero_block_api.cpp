@@ -258,9 +258,13 @@ int zero_block_norm_grad(const zero_block_norm_grad_args* g, void* ws, size_t ws
     a.format = g->format;
     a.accumulate = accumulate;
     a.gate_div = fast_div(static_cast<uint32_t>(a.plan.gate_rows));
+    // Only the sums that this call makes, one after the other from the start of
+    // ws: what it overwrites of a step's plan there then always includes the
+    // plan's signature, by which a step captured earlier knows that its table is gone.
+    const int64_t sums = a.plan.units * a.cols;
     a.sum_pre = static_cast<float*>(ws);
-    a.sum_post = a.sum_pre + a.plan.units * a.cols;
-    a.row_sums = a.sum_post + a.plan.units * a.cols;
+    a.sum_post = a.sum_pre + (given(g->dw_pre) ? sums : 0);
+    a.row_sums = a.sum_post + (given(g->dw_post) || (given(g->dgate) && a.plan.per_gate > 0) ? sums : 0);
     return hip_status(launch_block_norm_grad(a, stream));
 }
 

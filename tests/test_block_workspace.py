@@ -45,6 +45,13 @@ def test_a_step_after_a_call_on_its_workspace_uploads_its_table(host, what, whic
     assert after == first and plan and table
 
 
+@pytest.mark.parametrize("what,which,cols,gate_rows", CALLS)
+def test_a_call_that_overwrites_a_table_overwrites_its_signature(host, what, which, cols, gate_rows):
+    # a step that does not pass the host record (its launches were captured earlier) sees the signature alone
+    signature, table = host(what, which, cols, gate_rows, 0)[5:]
+    assert table or not signature
+
+
 def test_a_step_keeps_its_table_beside_a_call_on_another_workspace(host):
     for what, which, cols, gate_rows in CALLS:
         first, again, after, plan, table, _, _ = host(what, which, cols, gate_rows, 8 << 20)

@@ -85,3 +85,35 @@ def test_a_step_after_a_call_on_its_workspace(case):
     call(case, ws)
     assert step(ts, ws)["status"] == 0
     assert all(torch.equal(a, b) for a, b in zip(state(ts), state(want)))
+
+
+@pytest.mark.parametrize("case", CALLS)
+def test_a_captured_step_knows_that_its_table_is_gone(case):
+    ts, ws, res = tensors(), z.workspace(16 << 20), z.new_result()
+    hp = z.HParams(**HP)
+    z.zero_step(ts, hp, 0.0, ws, res)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z.zero_step(ts, hp, 0.0, ws, res)  # the table is in place: the graph holds the step alone
+    graph.replay()
+    assert z.read_result(res)["status"] == 0
+    before = state(ts)
+    call(case, ws)
+    if case[0] == () and case[2] == COLS:
+        return  # no sums: it writes nothing to its workspace
+    for _ in range(2):
+        graph.replay()
+        r = z.read_result(res)
+        assert r["status"] == z.ZERO_ERR_STALE_WORKSPACE and r["skipped"] == 1
+        assert all(torch.equal(a, b) for a, b in zip(state(ts), before))
+    z.zero_step(ts, hp, 0.0, ws, res)  # uploads the table again, for the graph too
+    assert z.read_result(res)["status"] == 0
+    for _ in range(2):
+        graph.replay()
+        assert z.read_result(res)["status"] == 0
+    want = tensors()
+    own = z.workspace(z.zero_step_workspace_bytes(want, 4, hp))
+    for _ in range(5):
+        step(want, own)
+    assert all(torch.equal(a, b) for a, b in zip(state(ts), state(want)))
