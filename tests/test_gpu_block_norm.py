@@ -166,6 +166,35 @@ def test_forward_does_not_depend_on_what_it_saves():
     assert torch.equal(keep[0], b.x_out) and torch.equal(keep[1], b.h)
 
 
+@pytest.mark.parametrize("cols", [64, 800])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_forward_settles_ties_whatever_it_saves(fmt, cols):
+    # As above: the fp32 product is the value itself, and the settled one is the
+    # next fp32 number towards zero, in nearly every column. An fp32 residual of
+    # zeros shows it as it is; h shows it where the product with a weight of
+    # 1 + 3/256 is the middle of two bf16 numbers (the values that are powers of two).
+    g = torch.Generator().manual_seed(cols)
+    unit, low, most = (16, 27, 31) if fmt == "e4m3" else (128, 221, 254)
+    n = torch.stack([integers_of_mean_square(g, cols, unit * unit, low, most) for _ in range(5)])
+    v = (torch.where(torch.rand(n.shape, generator=g) < 0.5, -1, 1) * n).float() / unit
+    settled = torch.nextafter(v, torch.zeros(()))
+    assert int((settled != v).sum()) > 0.9 * v.numel()
+    weight = 1 + 3.0 / 256
+    h = (settled * weight).bfloat16()
+    # the middle goes to the even number, 1 + 4/256, and what is below it to 1 + 2/256
+    assert int((h != (v * weight).bfloat16()).sum()) >= v.numel() // 50
+    x, one, w = v.to("cuda"), torch.ones(cols, device="cuda"), torch.full((cols,), weight, device="cuda")
+    new = lambda t=torch.float32: torch.empty(5, cols, dtype=t, device="cuda")  # noqa: E731
+    for saves in (True, False):
+        ck, rstd = (z.new_act8(5, cols, FORMATS[fmt]), torch.empty(5, device="cuda")) if saves else (None, None)
+        b = z.BlockNorm(x=torch.zeros_like(x), y=x.bfloat16(), w_post=one, x_out=new(), rstd_post=rstd, ckpt_post=ck, eps=2.0**-24)
+        z.zero_block_norm(b)
+        assert torch.equal(b.x_out.cpu(), settled), saves
+        b = z.BlockNorm(x=x, w_pre=w, h=new(torch.bfloat16), rstd_pre=rstd, ckpt_pre=ck, eps=2.0**-24)
+        z.zero_block_norm(b)
+        assert torch.equal(b.h.cpu(), h), saves
+
+
 def test_forward_in_place_and_nonfinite_rows():
     b, _ = forward(8, 200, resid=torch.float32)
     x = b.x.clone()
