@@ -52,8 +52,9 @@
  *    2^31 - 1 tiles (an update pass's tiles hold 2048 elements: about 4.4e12
  *    elements per call); a larger call is ZERO_ERR_INVALID_ARGUMENT.
  *  - Outputs must not alias inputs or each other, except the in-place
- *    master/exp_avg/exp_avg_sq and what an entry point allows. The library never advances `step`: the caller increments it
- *    when the result record says `skipped == 0`.
+ *    master/exp_avg/exp_avg_sq and what an entry point allows. The library
+ *    never advances `step`: the caller increments it when the result record
+ *    says `skipped == 0`.
  */
 #ifndef ZERO_STEP_H
 #define ZERO_STEP_H
@@ -642,8 +643,10 @@ int zero_offload_adamw_host(float* master, float* exp_avg, float* exp_avg_sq, co
  * buffers, which are then fp32; otherwise they are overwritten */
 #define ZERO_GRAD_ACCUMULATE 1
 
-/* Largest cols of zero_block_norm and zero_block_norm_grad, whose rows stay
- * in the registers of one workgroup. */
+/* Largest cols of zero_block_norm, whose rows stay in the registers of one
+ * workgroup, and of zero_block_norm_grad, which takes wider rows than those of
+ * 6144 columns (8192 from act8 buffers with few gate rows) in strips and reads
+ * them twice. */
 #define ZERO_BLOCK_NORM_MAX_COLS 16384
 
 /* A row-major matrix in device memory (the struct itself is host memory). */
@@ -706,10 +709,24 @@ int zero_act8_wgrad(const zero_rows* dy, const void* ckpt, int64_t rows, int64_t
  * Absent operands (data NULL): y (then x_out is x itself and is not written),
  * w_post (no norm after the block), gate (ones), w_pre (no norm before the
  * next block). rstd_post and rstd_pre (fp32, one per row) are the reciprocal
- * roots; ckpt_post and ckpt_pre the act8 buffers of yn and xn. Sums are held
- * in fp32 or more and every output is rounded once, the 8-bit codes from the
- * quotient rather than from its fp32 rounding. Two outputs at one address are
- * refused.
+ * roots; ckpt_post and ckpt_pre the act8 buffers of yn and xn. Two outputs at
+ * one address are refused.
+ *
+ * Rounding. Arithmetic is fp32, the mean of squares and its root fp64 from
+ * sums of squares in fp32 (at most two waves each). x_out and h are rounded to
+ * their own type once, at the end; the fp32 steps before that (the row's sum,
+ * the quotient, the products of residual_scale, gate and weight, the sum with
+ * x) are together within 56 * 2^-24 of the sum of the terms' magnitudes. The
+ * 8-bit codes are those of the quotient by the root in two fp32 parts, not of
+ * its fp32 rounding: an fp32 quotient that ends in 16 zero bits, as codes and
+ * the middles between them do, is moved one fp32 step towards the exact one, in
+ * x_out and h as in the codes and whether or not a checkpoint is written.
+ *
+ * Range. Where a row's squares pass the range of fp32 (some |z| of 2^64 or
+ * more) its reciprocal root is 0, and so is its n(z) (NaN where z is infinite).
+ * With eps 0, a row whose squares all vanish in fp32 (every |z| below 2^-75) has
+ * an infinite root, so that n(z) is infinite, or NaN where z is 0. A NaN in a
+ * row makes all of its n(z) NaN.
  */
 typedef struct zero_block_norm_args {
     int64_t rows;          /* 0 <= rows < 2^31 */
@@ -745,11 +762,16 @@ int zero_block_norm(const zero_block_norm_args* args, hipStream_t stream);
  * and, summed over rows in fp32 in an order that depends only on the sizes:
  *   dw_pre = sum dh * xn,   dw_post = sum g * d * yn,
  *   dgate[j] = sum over the rows of gate row j of residual_scale * d * w_post * yn.
+ * Arithmetic is fp32, and d enters dy and the sums as it is before the rounding
+ * to dx's type; each result is rounded to its own type once, at the end. Before
+ * that dx is within 112 * 2^-24 of the sum of its terms' magnitudes, dy within
+ * 224 * 2^-24, a sum over rows within (rows + 288) * 2^-24.
  * Absent (data NULL): dh (no norm before the next block; then dx_out is
  * given), dx_out (zeros), dy and what only it needs (no block output: dx
  * alone), and each of dw_pre, dw_post and dgate that is not wanted. dx may be
  * dx_out itself. Two outputs at one address are refused: where w_pre and w_post
- * are one vector, its two gradients still need a buffer each. rows == 0 writes zeros to dw_pre and dw_post.
+ * are one vector, its two gradients still need a buffer each. rows == 0 writes
+ * zeros to dw_pre and dw_post, or adds them.
  */
 typedef struct zero_block_norm_grad_args {
     int64_t rows;

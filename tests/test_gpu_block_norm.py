@@ -220,6 +220,35 @@ def test_forward_in_place_and_nonfinite_rows():
     assert torch.allclose(b.rstd_pre, torch.full_like(b.rstd_pre, 1e3))
 
 
+@pytest.mark.parametrize("cols", [40, 700, 9000])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_whose_squares_leave_the_range_of_fp32(dtype, cols):
+    # rows 0 .. 2: large squares, one infinite element, one NaN; rows 3 and 4: squares that vanish, with a zero among
+    # them; row 5: ordinary, near both ends of what a mean of squares can be
+    x = torch.ones(6, cols, device="cuda")
+    x[0] = -2.0**70
+    x[1, 7] = float("inf")
+    x[2, 11] = float("nan")
+    x[3] = 2.0**-80
+    x[4] = -2.0**-80
+    x[4, 3] = 0.0
+    for size in (2.0**55, 2.0**-55):
+        x[5] = size
+        x = x.to(dtype)
+        r = torch.zeros(6, device="cuda")
+        h, ck = torch.zeros(6, cols, dtype=torch.bfloat16, device="cuda"), z.new_act8(6, cols)
+        z.zero_block_norm(z.BlockNorm(x=x, w_pre=torch.ones(cols, device="cuda"), h=h, rstd_pre=r, ckpt_pre=ck, eps=0.0))
+        inf = float("inf")
+        assert torch.equal(r[[0, 1, 3, 4, 5]], torch.tensor([0, 0, inf, inf, 1 / size], device="cuda")) and bool(r[2].isnan())
+        assert not h[0].any() and bool(h[2].isnan().all()) and bool((h[3] == inf).all()) and bool((h[5] == 1).all())
+        other = torch.arange(cols, device="cuda")
+        assert bool(h[1, 7].isnan()) and not h[1][other != 7].any()
+        assert bool(h[4, 3].isnan()) and bool((h[4][other != 3] == -inf).all())
+        got = f64(decode_act8(ck)[0])
+        assert not got[0].any() and bool(got[2:5].isnan().all()) and bool((got[5] == 1).all())
+        assert bool(got[1, :32].isnan().all()) and not got[1, 32:].any()
+
+
 # ------------------------------------------------------------------ backward
 
 def backward(b, *, saved, grad=torch.float32, flags=0, dx_out=True, seed=7, pad=0, offset=0, wants=("dy", "dw_pre", "dw_post", "dgate")):
