@@ -3,15 +3,16 @@
 // the backward pass of the same, gfx950.
 //
 // A row stays in the registers of L lanes, V vectors of 8 columns a lane, so
-// every operand is read once and every result written once. Both are streams,
-// bound by HBM: with bf16 rows and both act8 buffers, 10.06 bytes a column
-// forwards and as many backwards. 16384 x 4096: forwards 123 to 131 us (5.2 to
-// 5.5 TB/s, where a copy of 2 GiB runs at 4.9), backwards 143 and 5 to join its
-// sums (4.7). 3001 x 5003 with fp32 rows: forwards 60 us (17 bytes a column and
-// a gate for every row, 4.2 TB/s), backwards 76 and 9 from rows as they are (18
-// bytes, 3.6 TB/s); their rows start anywhere in a line, and ten waves a
-// workgroup leave room for one on a compute unit. 128 x 768: 5.6, and 6.4 and
-// 3.4, the latency of a few rows in turn.
+// every operand is read once and every result written once (backwards, rows too
+// wide for that are read twice, see below). Both are streams, bound by HBM: with
+// bf16 rows and both act8 buffers, 10.06 bytes a column forwards and as many
+// backwards. 16384 x 4096: forwards 123 to 147 us (4.6 to 5.5 TB/s, where copies
+// run at 4.8 to 5.4), backwards 143 and 5 to join its sums (4.7). 3001 x 5003
+// with fp32 rows: forwards 60 us (14.06 bytes a column and 4 of a gate for every
+// row, 4.5 TB/s), backwards 76 and 9 from rows as they are (18 bytes, 3.6 TB/s);
+// their rows start anywhere in a line, and ten waves a workgroup leave room for
+// one on a compute unit. 128 x 768: 5.6, and 6.4 and 3.4, the latency of a few
+// rows in turn.
 #include "zero_act8_device.h"
 
 namespace zero {
@@ -668,9 +669,11 @@ static void norm_shape(NormArgs a, int64_t nv, hipStream_t s)
 // The outputs go past the caches at any size: 16384 x 4096 and the decoding of
 // its checkpoints 197 us instead of 223, 2048 x 4096 28.4 instead of 31.8, and
 // never slower. x and y do when what a call moves is more than the 256 MiB
-// Infinity Cache holds (16384 x 4096 172 instead of 197 us, 4096 x 4096 51.7
-// instead of 48.1) and their rows lie on 16 bytes: of others, neighbouring
-// loads share lines (6000 x 5003 158 instead of 146).
+// Infinity Cache holds and their rows lie on 16 bytes. Read past the caches and
+// through them, the decoding included: 16384 x 4096 197 us and 212, 8192 x 4096
+// 94 and 103, 6144 x 4096 72 and 76, about what the cache holds; below that 4096
+// x 4096 53 and 52 to 56, 2048 x 4096 32 and 30. 6000 x 5003, whose neighbouring
+// loads share lines, 151 and 154 on one machine, 158 and 146 on another.
 constexpr int64_t kInfinityCache = int64_t{256} << 20;
 
 static bool streams_inputs(const NormArgs& a)
@@ -685,8 +688,10 @@ hipError_t launch_block_norm(const NormArgs& args, hipStream_t s)
     NormArgs a = args;
     a.stream = streams_inputs(a);
     const int64_t nv = act8_pitch(a.cols) / 8;
-    // one vector a lane as long as a workgroup has the lanes: 8192 x 8192 with
-    // both reads 213 us, 231 with two; 3001 x 5003 81 and 102
+    // One vector a lane as long as a workgroup has the lanes: 8192 x 8192 with
+    // both reads 213 us, 231 with two; 3001 x 5003 81 and 102. Wider rows have
+    // nothing in flight across their sums: 8192 x 8192 146 us (4.6 TB/s),
+    // 4096 x 12288 148 (3.4), 2048 x 16384 93 (3.6).
     if (nv <= kWaveVecs) norm_shape<true, 1>(a, nv, s);
     else if (nv <= kMaxLanes) norm_shape<false, 1>(a, nv, s);
     else norm_shape<false, 2>(a, nv, s);
@@ -698,7 +703,10 @@ hipError_t launch_block_norm(const NormArgs& args, hipStream_t s)
 // Rows wider than 6144 columns go in strips of 4096, in two passes over them;
 // up to 8192 they still fit one workgroup if they come from 8 bits and there
 // are few gate rows (otherwise its registers do not hold what it needs). The
-// units are the same either way.
+// units are the same either way. From 8 bits and from rows as they are, in
+// TB/s of what has to be read and written once: 16384 x 4096 152 and 233 us (4.4
+// and 3.5), 8192 x 8192 162 and 422 (4.2 and 1.9), 4096 x 12288 215 and 310 (2.4
+// and 2.0).
 constexpr int kWideVecs = 768;
 constexpr int kStripLanes = 512;
 
@@ -708,13 +716,23 @@ NormGradPlan norm_grad_plan(int64_t rows, int64_t cols, int64_t gate_rows)
     const int64_t nv = act8_pitch(cols) / 8;
     p.gate_rows = gate_rows > 0 && gate_rows < rows ? gate_rows : (rows > 0 ? rows : 1);
     p.gates = (rows + p.gate_rows - 1) / p.gate_rows;
-    // As many units as run at once, 16 waves a compute unit, 12 of wide rows.
+    // Units of 16 waves a compute unit, of one workgroup of wide rows. Most of
+    // the kernels have 129 to 168 registers, which let 12 waves run at once (more
+    // registers 8, and 128 or fewer 16), so a large call goes in up to two rounds.
+    // Planned for 16, 12 and 8 waves, from 8 bits: 16384 x 4096 145, 142 and 141
+    // us, 65536 x 768 150, 118 and 142, 131072 x 512 166, 166 and 135, 3001 x 4096
+    // in gates of 700 43, 38 and 38.
     const int64_t waves = (nv + 63) / 64;
     int64_t target = kComputeUnits * (waves > 8 ? 1 : waves > 0 ? 16 / waves : 16);
     if (nv > kWideVecs) {
         p.strips = (nv + kStripLanes - 1) / kStripLanes;
         target = kComputeUnits * 2 / p.strips;
     }
+    // Whole gate rows a unit where they are more than the units: a little more
+    // than target of them leave nearly half the units without rows. 16384 x 4096
+    // from 8 bits: gates of 32 rows (512 units) 149 us, of 31 (265) 259, of 24
+    // (342) 212, of 16 (512) 153; 3001 x 5003 gates of 12 rows (251) 70 us, of 11
+    // (137) 95. Gates of one row 281 us, which read and write a gate for each.
     if (p.gates >= target) {
         p.unit_gates = (p.gates + target - 1) / target;
         p.units = (p.gates + p.unit_gates - 1) / p.unit_gates;

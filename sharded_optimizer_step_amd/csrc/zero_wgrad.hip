@@ -13,10 +13,11 @@
 // them: a wave decodes and stages a tile, then multiplies one, and the two
 // waves of a SIMD do so nearly together; at the 2.0 to 2.1 GHz that the chip
 // holds under this load. 8192 tokens: 11008 x 4096 from e4m3 to bf16 648 us
-// (1.14 PFLOP/s; 2.7 rounds of tiles), 4096 x 4096 from int8 added to fp32 271
-// us (1.01; 27 of them the 134 MB of dW read and written at the rate of a
-// copy). Small ones are bound by a tile's start and the latency of its steps:
-// 192 tokens and 768 x 768 5.6 us.
+// (1.14 PFLOP/s; 2.7 rounds of tiles); 4096 x 4096 from int8, with inputs that do
+// not lie in the caches, 248 us to bf16 (1.11), 255 to fp32 and 271 added to
+// fp32 (1.01; 134 MB of dW read and written instead of 34 written). Small ones
+// are bound by a tile's start and the latency of its steps: 192 tokens and
+// 768 x 768 5.6 us.
 #include "zero_act8_device.h"
 
 namespace zero {
@@ -427,11 +428,17 @@ constexpr Candidate candidate(int tile, double alone, double full)
 // expected to take: rounds of workgroups through the chip, each of them a
 // start and its tokens, and for split tiles their parts written, read and
 // joined by a second launch. Either no tile is whole, or as many as fill whole
-// rounds, or all. Measured: 8192 tokens and 4096 x 4096 take 211 us with
-// 256 x 256 tiles, 290 with 128 x 128, 484 with 64 x 64; 1024 tokens and
-// 768 x 768 23, 16 and 9.2 us; 30011 tokens and 200 x 333 unsplit 698, 420 and
-// 218 us, split 30, 26 and 24 us; a million tokens and 64 x 64 78 us in 128
-// ranges, 43 in 768.
+// rounds, or all. Measured: 8192 tokens and 4096 x 4096 take 240 us with
+// 256 x 256 tiles, 307 with 128 x 128, 512 with 64 x 64; 1024 tokens and
+// 768 x 768 33, 20 and 13 us; 30011 tokens and 200 x 333 unsplit 692, 393 and
+// 254 us, split 31, 25 and 22 us; a million tokens and 64 x 64 106 us in 128
+// ranges, 50 in 768.
+//
+// A step's times are differences of two lengths, e4m3 to bf16: one tile, and one
+// as many as the chip holds. (Taken again, over 64 and 192 steps: 0.72 and 0.83,
+// 0.89 and 1.10, 0.59 and 0.81 us.) The model knows nothing of the epilogue, nor
+// of what the caches hold: it says 227 us of the 4096 x 4096 above and 29 of
+// 30011 x 200 x 333, which take 240 and 22. It only has to order the candidates.
 WgradPlan wgrad_plan(int64_t rows, int64_t outs, int64_t cols)
 {
     static const Candidate kTiles[] = {candidate<TileBig>(0, 0.80, 0.87), candidate<TileMid>(1, 0.95, 1.18),

@@ -69,3 +69,18 @@ def test_norms_keep_the_waves_their_split_counts_on(usage):
         m = re.search(r"block_norm_grad_kernelILb(\d)ELi(\d+)ELb(\d)ELb(\d)ELb(\d)ELb(\d)E", name)
         if m:
             assert int(u["Occupancy"]) * 4 >= int(m.group(2)) // 64, (name, u)  # its largest workgroup starts
+
+
+def test_norm_gradients_run_the_waves_that_their_split_is_measured_with(usage):
+    # 12 waves a compute unit (168 registers); 8 of some kernels for rows as they are with many gate rows; the kernels of
+    # 16-wave workgroups need 16
+    seen = 0
+    for name, u in usage.items():
+        m = re.search(r"block_norm_grad_kernelILb(\d)ELi(\d+)ELb(\d)ELb(\d)ELb(\d)ELb(\d)E", name)
+        if m is None:
+            continue
+        seen += 1
+        most, coded, many = int(m.group(2)), m.group(4) == "1", m.group(5) == "1"
+        waves = 4 * int(u["Occupancy"])
+        assert waves >= (16 if most == 1024 else 8 if many and not coded else 12), (name, u)
+    assert seen == 34  # as grad_shape and grad_split make them
