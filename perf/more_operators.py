@@ -353,6 +353,16 @@ def _plain_ffn(s):
     return out
 
 
+def _bf16(x):
+    """64-bit values to the nearest bf16. By way of fp32, so one that this moves
+    onto the middle of two bf16 values is moved back off it first."""
+    f = x.float()
+    bits = f.view(torch.int32)
+    middle = ((bits & 0xFFFF) == 0x8000) & (f.double() != x)
+    toward = torch.where(f.double().abs() > x.abs(), -1, 1).to(torch.int32)
+    return torch.where(middle, bits + toward, bits).view(torch.float32).to(torch.bfloat16)
+
+
 def _plain_ffn_grad(s):
     rows, hidden, cols = s["rows"], s["hidden"], s["cols"]
     if s["saved"] == "raw":
@@ -363,7 +373,7 @@ def _plain_ffn_grad(s):
     # last bit next to the border of two values would count for 2^-8
     da, g, u = s["da"].double(), g.double(), u.double()
     f, df = _act(g, s["act"])
-    out = dict(dgate=(da * u * df).to(torch.bfloat16), dup=(da * f).to(torch.bfloat16))
+    out = dict(dgate=_bf16(da * u * df), dup=_bf16(da * f))
     dg, du = out["dgate"].float(), out["dup"].float()  # the products are those of the stored gradients
     out["dh"] = (dg @ s["w_gate"].float() + du @ s["w_up"].float()).to(torch.bfloat16)
     x = s["h"].float() if s["input"] == "raw" else _decode(s["saved_h"], rows, cols, s["fmt"]) * s["scale"].float()
@@ -588,7 +598,7 @@ def exact(case, seed):
     if case["again"]:
         out["read_a"] = _nearest64(f * u, fmt)
     # the gradients are stored in bf16, and what follows is taken from them
-    dg, du = (out[n].to(torch.bfloat16).double() for n in ("dgate", "dup"))
+    dg, du = (torch.ldexp(torch.round(torch.frexp(out[n])[0] * 256) / 256, torch.frexp(out[n])[1]) for n in ("dgate", "dup"))
     out["dh"] = torch.mm(dg, wg).addmm_(du, wu)
     x = s["h"].double() if case["input"] == "raw" else _read64(s["saved_h"], rows, cols, fmt) * s["scale"].double()
     out["dw_gate"], out["dw_up"] = old("dw_gate") + torch.mm(dg.t(), x), old("dw_up") + torch.mm(du.t(), x)
