@@ -639,14 +639,16 @@ int zero_offload_adamw_host(float* master, float* exp_avg, float* exp_avg_sq, co
 #define ZERO_ACT8_E4M3 1
 #define ZERO_ACT8_INT8 2
 
-/* flag of zero_act8_wgrad and zero_block_norm_grad: add to the gradient
- * buffers, which are then fp32; otherwise they are overwritten */
+/* flag of zero_act8_wgrad, zero_block_norm_grad, zero_layer_norm_grad and
+ * zero_block_ffn_grad: add to the gradient buffers, which are then fp32;
+ * otherwise they are overwritten */
 #define ZERO_GRAD_ACCUMULATE 1
 
-/* Largest cols of zero_block_norm, whose rows stay in the registers of one
- * workgroup, and of zero_block_norm_grad, which takes wider rows than those of
- * 6144 columns (8192 from act8 buffers with few gate rows) in strips and reads
- * them twice. */
+/* Largest cols of zero_block_norm and zero_layer_norm, whose rows stay in the
+ * registers of one workgroup, and of zero_block_norm_grad and
+ * zero_layer_norm_grad, which take wider rows than those of 6144 columns (8192
+ * from act8 buffers with few gate rows), the latter than those of 8192, in
+ * strips and read them twice. */
 #define ZERO_BLOCK_NORM_MAX_COLS 16384
 
 /* A row-major matrix in device memory (the struct itself is host memory). */
@@ -807,6 +809,186 @@ size_t zero_block_norm_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t 
  * run concurrently. The plan that a step keeps in any part of it is forgotten,
  * as by zero_workspace_forget. */
 int zero_block_norm_grad(const zero_block_norm_grad_args* args, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * zero_layer_norm -- the residual add and the layer norm before a block, in
+ * one pass. Per row of cols values:
+ *   x_out = x + y                       (stored in x's type)
+ *   mean  = sum(x_out) / cols           of x_out as stored
+ *   rstd  = 1 / sqrt(sum((x_out - mean)^2) / cols + eps)
+ *   xn    = (x_out - mean) * rstd
+ *   h     = w * xn + b
+ * Absent operands (data NULL): y (then x_out is x itself and is not written),
+ * w (ones), b (zeros). mean and rstd (fp32, one per row) are optional;
+ * ckpt_xn is the act8 buffer of xn, from which zero_layer_norm_grad can take
+ * it, and ckpt_h that of h before its rounding to bf16, from which
+ * zero_act8_wgrad and zero_block_ffn_grad take the gradients of what h goes
+ * into. x_out may be x itself; two outputs at one address are refused.
+ *
+ * Rounding. Arithmetic is fp32. The mean is taken in two steps, a first one and
+ * the mean difference to it, and the squares about it, so that rows far from 0
+ * keep their variance. With f = 1 + 22 * 2^-24 * mean(|x_out|) * rstd, xn is
+ * within 100 * 2^-24 * (|xn| + f), rstd within 100 * 2^-24 * f of itself, mean
+ * within 84 * 2^-24 * mean(|x_out|); each result is then rounded to its own type
+ * once.
+ *
+ * Range. A row with an inf or NaN, or whose sum passes fp32's range, has NaN in
+ * its mean, rstd, xn and h; one whose squares pass it has rstd 0. With eps 0 a
+ * row of equal values has a large or infinite rstd, and anything in xn.
+ */
+typedef struct zero_layer_norm_args {
+    int64_t rows;     /* 0 <= rows < 2^31 */
+    int64_t cols;     /* 0 <= cols <= ZERO_BLOCK_NORM_MAX_COLS */
+    double eps;       /* finite, >= 0; rounded to fp32 */
+    zero_rows x;      /* residual stream, bf16 or fp32 */
+    zero_rows y;      /* what is added to it, bf16 */
+    zero_rows w;      /* cols, bf16 or fp32 */
+    zero_rows b;      /* cols, bf16 or fp32 */
+    zero_rows x_out;  /* the type of x; written with y, may be x itself */
+    zero_rows h;      /* bf16 */
+    float* mean;      /* rows, or NULL */
+    float* rstd;      /* rows, or NULL */
+    void* ckpt_xn;    /* act8 buffer, or NULL */
+    void* ckpt_h;     /* act8 buffer, or NULL */
+    int32_t format;   /* of both act8 buffers */
+    int32_t reserved; /* must be 0 */
+} zero_layer_norm_args;
+
+int zero_layer_norm(const zero_layer_norm_args* args, hipStream_t stream);
+
+/*
+ * zero_layer_norm_grad -- the gradients of zero_layer_norm. xn comes from an
+ * act8 buffer, or (ckpt_xn NULL) from x_out, mean and rstd. With v = w * dh,
+ * per row:
+ *   dx = dx_out + rstd * (v - mean(v) - xn * mean(v * xn))
+ * which is the gradient of both x and y; dy is the same values in bf16, for a
+ * block whose output y is bf16 beside an fp32 residual stream. Summed over rows
+ * in fp32 in an order that depends only on the sizes:
+ *   dw = sum dh * xn,   db = sum dh.
+ * Absent (data NULL): dx_out (zeros), w (ones), and each of dy, dw and db that
+ * is not wanted. dx may be dx_out itself. Two outputs at one address are
+ * refused. rows == 0 writes zeros to dw and db, or adds them.
+ */
+typedef struct zero_layer_norm_grad_args {
+    int64_t rows;
+    int64_t cols;
+    zero_rows dh;        /* gradient of h, bf16 */
+    zero_rows dx_out;    /* gradient of x_out from what follows, the type of dx */
+    zero_rows w;         /* as in zero_layer_norm */
+    zero_rows x_out;     /* when ckpt_xn is NULL: the type of dx */
+    const float* mean;   /* rows, when ckpt_xn is NULL */
+    const float* rstd;   /* rows */
+    const void* ckpt_xn; /* act8 buffer of xn, or NULL */
+    zero_rows dx;        /* bf16 or fp32 */
+    zero_rows dy;        /* bf16 */
+    zero_rows dw;        /* cols, bf16 or fp32 */
+    zero_rows db;        /* cols, bf16 or fp32 */
+    int32_t format;      /* of the act8 buffer */
+    int32_t flags;       /* ZERO_GRAD_ACCUMULATE: dw and db are fp32 and added to */
+} zero_layer_norm_grad_args;
+
+/* Workspace size of zero_layer_norm_grad (partial column sums); 0 on invalid
+ * sizes. */
+size_t zero_layer_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
+
+/* ws: as in zero_block_norm_grad. */
+int zero_layer_norm_grad(const zero_layer_norm_grad_args* args, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The gated feed-forward block of a layer, from its normalised input to what
+ * goes into its down projection:
+ *   gate = h * w_gate^T,   up = h * w_up^T,   a = act(gate) * up
+ * with h rows x cols and the two weights hidden x cols, all bf16.
+ */
+#define ZERO_FFN_SILU 1      /* g / (1 + exp(-g)) */
+#define ZERO_FFN_GELU 2      /* g * (1 + erf(g / sqrt(2))) / 2 */
+#define ZERO_FFN_GELU_TANH 3 /* g * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))) / 2 */
+
+/*
+ * zero_block_ffn -- both projections, the activation and the product in one
+ * kernel. gate and up are summed in fp32 in an order that depends only on the
+ * sizes, and a is made from these sums. For the backward pass they can be kept
+ * as bf16 rows (gate, up) or as act8 buffers (ckpt_gate, ckpt_up), or neither;
+ * each result is rounded to its own type once. cols == 0: the sums are 0.
+ * rows < 2^31, cols and hidden <= 2^30, rows times either (rounded up to 32)
+ * < 2^36, and fewer than 2^20 tiles of 128 x 128 of rows x hidden, rows x cols
+ * and hidden x cols. Two outputs at one address are refused.
+ */
+typedef struct zero_block_ffn_args {
+    int64_t rows;
+    int64_t cols;
+    int64_t hidden;
+    zero_rows h;      /* rows x cols, bf16 */
+    zero_rows w_gate; /* hidden x cols, bf16 */
+    zero_rows w_up;   /* hidden x cols, bf16 */
+    zero_rows a;      /* rows x hidden, bf16 */
+    zero_rows gate;   /* rows x hidden, bf16, or absent */
+    zero_rows up;     /* rows x hidden, bf16, or absent */
+    void* ckpt_gate;  /* act8 buffer of rows x hidden, or NULL */
+    void* ckpt_up;    /* act8 buffer of rows x hidden, or NULL */
+    int32_t format;   /* of both act8 buffers */
+    int32_t act;      /* ZERO_FFN_* */
+} zero_block_ffn_args;
+
+/* Workspace size of zero_block_ffn (partial sums where few rows leave the
+ * chip's units to the summed columns; often 0); 0 on invalid sizes. */
+size_t zero_block_ffn_workspace_bytes(int64_t rows, int64_t cols, int64_t hidden);
+
+/* ws: as in zero_act8_wgrad. */
+int zero_block_ffn(const zero_block_ffn_args* args, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * zero_block_ffn_grad -- the gradients of zero_block_ffn from da, the gradient
+ * of a, and the saved gate and up: bf16 rows, or act8 buffers.
+ *   dgate = da * up * act'(gate),   dup = da * act(gate)        (bf16)
+ *   dh      = dgate * w_gate + dup * w_up
+ *   dw_gate (+)= dgate^T * h,   dw_up (+)= dup^T * h
+ * dgate and dup are the nearest bf16 values of the formulas (computed in fp32,
+ * and in fp64 where that leaves the rounding open); dh and the weight gradients
+ * are those of dgate and dup as stored, summed in fp32 in an order that depends
+ * only on the sizes, each rounded to its own type once.
+ * The block's input comes as bf16 rows h, or as the act8 buffer ckpt_h whose
+ * decoded columns are multiplied with col_scale (cols values, bf16 or fp32;
+ * absent: ones), as in zero_act8_wgrad. ckpt_a, if given, is written: the act8
+ * buffer of act(gate) * up, for the weight gradient of the down projection
+ * without a kept from the forward pass.
+ * Absent (data NULL): dh with w_gate and w_up, and each of dw_gate and dw_up
+ * that is not wanted; without both, h, ckpt_h and col_scale. Two outputs at one
+ * address are refused. rows == 0 writes zeros to dw_gate and dw_up, or adds
+ * them; hidden == 0 writes zeros to dh. Sizes as in zero_block_ffn.
+ */
+typedef struct zero_block_ffn_grad_args {
+    int64_t rows;
+    int64_t cols;
+    int64_t hidden;
+    zero_rows da;          /* rows x hidden, bf16 */
+    zero_rows gate;        /* rows x hidden, bf16, when ckpt_gate is NULL */
+    zero_rows up;          /* rows x hidden, bf16, when ckpt_up is NULL */
+    const void* ckpt_gate; /* act8 buffers, both or neither */
+    const void* ckpt_up;
+    zero_rows w_gate;      /* hidden x cols, bf16, with dh */
+    zero_rows w_up;        /* hidden x cols, bf16, with dh */
+    zero_rows h;           /* rows x cols, bf16, when a weight gradient is wanted and ckpt_h is NULL */
+    const void* ckpt_h;    /* act8 buffer of rows x cols, or NULL */
+    zero_rows col_scale;   /* cols, bf16 or fp32, with ckpt_h */
+    zero_rows dgate;       /* rows x hidden, bf16, written */
+    zero_rows dup;         /* rows x hidden, bf16, written */
+    zero_rows dh;          /* rows x cols, bf16 */
+    zero_rows dw_gate;     /* hidden x cols, bf16 or fp32 */
+    zero_rows dw_up;       /* hidden x cols, bf16 or fp32 */
+    void* ckpt_a;          /* act8 buffer of rows x hidden, written, or NULL */
+    int32_t format;        /* of all act8 buffers */
+    int32_t act;           /* ZERO_FFN_* */
+    int32_t flags;         /* ZERO_GRAD_ACCUMULATE: dw_gate and dw_up are fp32 and added to */
+    int32_t reserved;      /* must be 0 */
+} zero_block_ffn_grad_args;
+
+/* Workspace size of zero_block_ffn_grad, whichever of its gradients are wanted
+ * and however h comes; 0 on invalid sizes. */
+size_t zero_block_ffn_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t hidden);
+
+/* ws: as in zero_act8_wgrad. */
+int zero_block_ffn_grad(const zero_block_ffn_grad_args* args, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * zero_workspace_forget -- drop the host-side record that `ws` holds the

@@ -41,6 +41,12 @@ Functions keep the C names:
 * ``zero_block_norm(BlockNorm(...))``, ``zero_block_norm_grad_workspace_bytes(rows, cols, gate_rows)``,
   ``zero_block_norm_grad(BlockNormGrad(...), flags, ws)``: the norms after a block and before the next one, fused
   with the block's gate, the residual scale and the residual add, forward and backward
+* ``zero_layer_norm(LayerNorm(...))``, ``zero_layer_norm_grad_workspace_bytes(rows, cols)``,
+  ``zero_layer_norm_grad(LayerNormGrad(...), flags, ws)``: the residual add and the layer norm before a block, forward
+  and backward
+* ``zero_block_ffn_workspace_bytes(rows, cols, hidden)``, ``zero_block_ffn(BlockFfn(...), ws)``,
+  ``zero_block_ffn_grad_workspace_bytes(rows, cols, hidden)``, ``zero_block_ffn_grad(BlockFfnGrad(...), flags, ws)``:
+  the gated feed-forward block's two projections, activation and product in one kernel, and all gradients of it
 * ``zero_workspace_forget(ws)``, ``zero_status_string(status)``
 """
 from __future__ import annotations
@@ -76,6 +82,9 @@ ACT8_E4M3 = 1
 ACT8_INT8 = 2
 GRAD_ACCUMULATE = 1
 BLOCK_NORM_MAX_COLS = 16384
+FFN_SILU = 1
+FFN_GELU = 2
+FFN_GELU_TANH = 3
 
 # Every symbol the C ABI exports (include/zero_step.h).
 EXPORTS = ("zero_shard_reduce", "zero_grad_check_norm_workspace_bytes", "zero_grad_check_norm", "zero_adamw_step",
@@ -87,7 +96,9 @@ EXPORTS = ("zero_shard_reduce", "zero_grad_check_norm_workspace_bytes", "zero_gr
            "zero_offload_step_amp", "zero_workspace_forget", "zero_status_string", "zero_step_noalloc",
            "zero_bucket_step_workspace_bytes", "zero_bucket_step", "zero_act8_bytes", "zero_act8_save",
            "zero_act8_load", "zero_act8_wgrad_workspace_bytes", "zero_act8_wgrad", "zero_block_norm",
-           "zero_block_norm_grad_workspace_bytes", "zero_block_norm_grad")
+           "zero_block_norm_grad_workspace_bytes", "zero_block_norm_grad", "zero_layer_norm",
+           "zero_layer_norm_grad_workspace_bytes", "zero_layer_norm_grad", "zero_block_ffn_workspace_bytes",
+           "zero_block_ffn", "zero_block_ffn_grad_workspace_bytes", "zero_block_ffn_grad")
 LOSS_SCALE_BYTES = 16
 
 
@@ -153,6 +164,36 @@ class _CBlockNormGrad(ctypes.Structure):
                 ("ckpt_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p), ("rstd_post", ctypes.c_void_p),
                 ("dx", _CRows), ("dy", _CRows), ("dw_pre", _CRows), ("dw_post", _CRows), ("dgate", _CRows),
                 ("format", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class _CLayerNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("eps", ctypes.c_double), ("x", _CRows),
+                ("y", _CRows), ("w", _CRows), ("b", _CRows), ("x_out", _CRows), ("h", _CRows),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("ckpt_xn", ctypes.c_void_p),
+                ("ckpt_h", ctypes.c_void_p), ("format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _CLayerNormGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dh", _CRows), ("dx_out", _CRows), ("w", _CRows),
+                ("x_out", _CRows), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("ckpt_xn", ctypes.c_void_p),
+                ("dx", _CRows), ("dy", _CRows), ("dw", _CRows), ("db", _CRows), ("format", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
+
+
+class _CBlockFfn(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("hidden", ctypes.c_int64), ("h", _CRows),
+                ("w_gate", _CRows), ("w_up", _CRows), ("a", _CRows), ("gate", _CRows), ("up", _CRows),
+                ("ckpt_gate", ctypes.c_void_p), ("ckpt_up", ctypes.c_void_p), ("format", ctypes.c_int32),
+                ("act", ctypes.c_int32)]
+
+
+class _CBlockFfnGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("hidden", ctypes.c_int64), ("da", _CRows),
+                ("gate", _CRows), ("up", _CRows), ("ckpt_gate", ctypes.c_void_p), ("ckpt_up", ctypes.c_void_p),
+                ("w_gate", _CRows), ("w_up", _CRows), ("h", _CRows), ("ckpt_h", ctypes.c_void_p),
+                ("col_scale", _CRows), ("dgate", _CRows), ("dup", _CRows), ("dh", _CRows), ("dw_gate", _CRows),
+                ("dw_up", _CRows), ("ckpt_a", ctypes.c_void_p), ("format", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("flags", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class ZeroError(RuntimeError):
@@ -246,6 +287,20 @@ def lib() -> ctypes.CDLL:
         L.zero_block_norm_grad_workspace_bytes.restype = sz
         L.zero_block_norm_grad.argtypes = [vp, vp, sz, vp]
         L.zero_block_norm_grad.restype = ctypes.c_int
+        L.zero_layer_norm.argtypes = [vp, vp]
+        L.zero_layer_norm.restype = ctypes.c_int
+        L.zero_layer_norm_grad_workspace_bytes.argtypes = [i64, i64]
+        L.zero_layer_norm_grad_workspace_bytes.restype = sz
+        L.zero_layer_norm_grad.argtypes = [vp, vp, sz, vp]
+        L.zero_layer_norm_grad.restype = ctypes.c_int
+        L.zero_block_ffn_workspace_bytes.argtypes = [i64, i64, i64]
+        L.zero_block_ffn_workspace_bytes.restype = sz
+        L.zero_block_ffn.argtypes = [vp, vp, sz, vp]
+        L.zero_block_ffn.restype = ctypes.c_int
+        L.zero_block_ffn_grad_workspace_bytes.argtypes = [i64, i64, i64]
+        L.zero_block_ffn_grad_workspace_bytes.restype = sz
+        L.zero_block_ffn_grad.argtypes = [vp, vp, sz, vp]
+        L.zero_block_ffn_grad.restype = ctypes.c_int
         L.zero_workspace_forget.argtypes = [vp]
         L.zero_workspace_forget.restype = ctypes.c_int
         L.zero_status_string.argtypes = [ctypes.c_int]
@@ -922,6 +977,10 @@ def new_act8(rows: int, cols: int, format: int = ACT8_E4M3, device=None) -> Act8
 _ROWS = struct.Struct("=QqiI")
 _BLOCK_NORM = struct.Struct("=qqqdd" + "QqiI" * 7 + "QQQQii")
 _BLOCK_NORM_GRAD = struct.Struct("=qqqd" + "QqiI" * 7 + "QQQQ" + "QqiI" * 5 + "ii")
+_LAYER_NORM = struct.Struct("=qqd" + "QqiI" * 6 + "QQQQii")
+_LAYER_NORM_GRAD = struct.Struct("=qq" + "QqiI" * 4 + "QQQ" + "QqiI" * 4 + "ii")
+_BLOCK_FFN = struct.Struct("=qqq" + "QqiI" * 6 + "QQii")
+_BLOCK_FFN_GRAD = struct.Struct("=qqq" + "QqiI" * 3 + "QQ" + "QqiI" * 3 + "Q" + "QqiI" * 6 + "Qiiii")
 _ABSENT = (0, 0, 0, 0)
 
 
@@ -1164,6 +1223,168 @@ def zero_block_norm_grad(b: BlockNormGrad, flags: int = 0, ws: Optional[torch.Te
         *_vector(b.dw_pre, "dw_pre", cols, dev), *_vector(b.dw_post, "dw_post", cols, dev),
         *_row_major(b.dgate, "dgate", gates, cols, dev), _act8_format(b.ckpt_post, b.ckpt_pre), flags)
     _check(lib().zero_block_norm_grad(args, wsp, wsb, _stream_of(stream, dev)), "zero_block_norm_grad")
+
+
+@dataclasses.dataclass
+class LayerNorm:
+    """The operands of zero_layer_norm; None is an absent one. x and x_out: the
+    residual stream (bf16 or fp32); y and h: bf16; w and b: bf16 or fp32; mean
+    and rstd: fp32; ckpt_*: Act8 of one format."""
+    x: torch.Tensor
+    h: torch.Tensor
+    y: Optional[torch.Tensor] = None
+    w: Optional[torch.Tensor] = None
+    b: Optional[torch.Tensor] = None
+    x_out: Optional[torch.Tensor] = None
+    mean: Optional[torch.Tensor] = None
+    rstd: Optional[torch.Tensor] = None
+    ckpt_xn: Optional[Act8] = None
+    ckpt_h: Optional[Act8] = None
+    eps: float = 1e-5
+
+
+@dataclasses.dataclass
+class LayerNormGrad:
+    """The operands of zero_layer_norm_grad; None is an absent one. The
+    normalised rows come from ckpt_xn or, without it, from x_out and mean."""
+    dx: torch.Tensor
+    dh: torch.Tensor
+    rstd: torch.Tensor
+    dx_out: Optional[torch.Tensor] = None
+    w: Optional[torch.Tensor] = None
+    x_out: Optional[torch.Tensor] = None
+    mean: Optional[torch.Tensor] = None
+    ckpt_xn: Optional[Act8] = None
+    dy: Optional[torch.Tensor] = None
+    dw: Optional[torch.Tensor] = None
+    db: Optional[torch.Tensor] = None
+
+
+def zero_layer_norm(b: LayerNorm, stream=None) -> None:
+    rows, cols, dev = _matrix(b.x, "x")
+    bf16 = torch.bfloat16
+    args = _LAYER_NORM.pack(
+        rows, cols, b.eps, *_row_major(b.x, "x", rows, cols, dev), *_row_major(b.y, "y", rows, cols, dev, bf16),
+        *_vector(b.w, "w", cols, dev), *_vector(b.b, "b", cols, dev),
+        *_row_major(b.x_out, "x_out", rows, cols, dev, b.x.dtype), *_row_major(b.h, "h", rows, cols, dev, bf16),
+        _per_row(b.mean, "mean", rows, dev), _per_row(b.rstd, "rstd", rows, dev),
+        _act8(b.ckpt_xn, "ckpt_xn", rows, cols, dev), _act8(b.ckpt_h, "ckpt_h", rows, cols, dev),
+        _act8_format(b.ckpt_xn, b.ckpt_h), 0)
+    _check(lib().zero_layer_norm(args, _stream_of(stream, dev)), "zero_layer_norm")
+
+
+def zero_layer_norm_grad_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().zero_layer_norm_grad_workspace_bytes(int(rows), int(cols)))
+
+
+def zero_layer_norm_grad(b: LayerNormGrad, flags: int = 0, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    rows, cols, dev = _matrix(b.dx, "dx")
+    bf16, like = torch.bfloat16, b.dx.dtype
+    wsp, wsb = _workspace_of(ws, dev)
+    args = _LAYER_NORM_GRAD.pack(
+        rows, cols, *_row_major(b.dh, "dh", rows, cols, dev, bf16), *_row_major(b.dx_out, "dx_out", rows, cols, dev, like),
+        *_vector(b.w, "w", cols, dev), *_row_major(b.x_out, "x_out", rows, cols, dev, like),
+        _per_row(b.mean, "mean", rows, dev), _per_row(b.rstd, "rstd", rows, dev),
+        _act8(b.ckpt_xn, "ckpt_xn", rows, cols, dev), *_row_major(b.dx, "dx", rows, cols, dev),
+        *_row_major(b.dy, "dy", rows, cols, dev, bf16), *_vector(b.dw, "dw", cols, dev), *_vector(b.db, "db", cols, dev),
+        _act8_format(b.ckpt_xn, None), flags)
+    _check(lib().zero_layer_norm_grad(args, wsp, wsb, _stream_of(stream, dev)), "zero_layer_norm_grad")
+
+
+@dataclasses.dataclass
+class BlockFfn:
+    """The operands of zero_block_ffn, all bf16; None is an absent one. gate
+    and up, or ckpt_gate and ckpt_up (Act8 of one format): what the backward
+    pass reads. act: FFN_SILU, FFN_GELU or FFN_GELU_TANH."""
+    h: torch.Tensor
+    w_gate: torch.Tensor
+    w_up: torch.Tensor
+    a: torch.Tensor
+    gate: Optional[torch.Tensor] = None
+    up: Optional[torch.Tensor] = None
+    ckpt_gate: Optional[Act8] = None
+    ckpt_up: Optional[Act8] = None
+    act: int = FFN_SILU
+
+
+@dataclasses.dataclass
+class BlockFfnGrad:
+    """The operands of zero_block_ffn_grad; None is an absent one. The saved
+    gate and up come as bf16 rows or Act8, and so does the block's input (h, or
+    ckpt_h with col_scale); all Act8 are of one format. dw_gate and dw_up: bf16
+    or fp32."""
+    da: torch.Tensor
+    dgate: torch.Tensor
+    dup: torch.Tensor
+    gate: Optional[torch.Tensor] = None
+    up: Optional[torch.Tensor] = None
+    ckpt_gate: Optional[Act8] = None
+    ckpt_up: Optional[Act8] = None
+    w_gate: Optional[torch.Tensor] = None
+    w_up: Optional[torch.Tensor] = None
+    dh: Optional[torch.Tensor] = None
+    h: Optional[torch.Tensor] = None
+    ckpt_h: Optional[Act8] = None
+    col_scale: Optional[torch.Tensor] = None
+    dw_gate: Optional[torch.Tensor] = None
+    dw_up: Optional[torch.Tensor] = None
+    ckpt_a: Optional[Act8] = None
+    act: int = FFN_SILU
+
+
+def zero_block_ffn_workspace_bytes(rows: int, cols: int, hidden: int) -> int:
+    return int(lib().zero_block_ffn_workspace_bytes(int(rows), int(cols), int(hidden)))
+
+
+def zero_block_ffn(b: BlockFfn, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    rows, cols, dev = _matrix(b.h, "h")
+    hidden = _matrix(b.w_gate, "w_gate")[0]
+    bf16 = torch.bfloat16
+    wsp, wsb = _workspace_of(ws, dev)
+    args = _BLOCK_FFN.pack(
+        rows, cols, hidden, *_row_major(b.h, "h", rows, cols, dev, bf16),
+        *_row_major(b.w_gate, "w_gate", hidden, cols, dev, bf16), *_row_major(b.w_up, "w_up", hidden, cols, dev, bf16),
+        *_row_major(b.a, "a", rows, hidden, dev, bf16), *_row_major(b.gate, "gate", rows, hidden, dev, bf16),
+        *_row_major(b.up, "up", rows, hidden, dev, bf16), _act8(b.ckpt_gate, "ckpt_gate", rows, hidden, dev),
+        _act8(b.ckpt_up, "ckpt_up", rows, hidden, dev), _act8_format(b.ckpt_gate, b.ckpt_up), b.act)
+    _check(lib().zero_block_ffn(args, wsp, wsb, _stream_of(stream, dev)), "zero_block_ffn")
+
+
+def zero_block_ffn_grad_workspace_bytes(rows: int, cols: int, hidden: int) -> int:
+    return int(lib().zero_block_ffn_grad_workspace_bytes(int(rows), int(cols), int(hidden)))
+
+
+def _ffn_cols(b: BlockFfnGrad) -> int:
+    """The width of the block's input, from the operands that have it."""
+    for t in (b.dh, b.dw_gate, b.dw_up):
+        if t is not None:
+            return _matrix(t, "dh, dw_gate or dw_up")[1]
+    return 0
+
+
+def zero_block_ffn_grad(b: BlockFfnGrad, flags: int = 0, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    rows, hidden, dev = _matrix(b.da, "da")
+    cols = _ffn_cols(b)
+    bf16 = torch.bfloat16
+    wsp, wsb = _workspace_of(ws, dev)
+    wide = lambda t, name: _row_major(t, name, rows, hidden, dev, bf16)  # noqa: E731
+    args = _BLOCK_FFN_GRAD.pack(
+        rows, cols, hidden, *wide(b.da, "da"), *wide(b.gate, "gate"), *wide(b.up, "up"),
+        _act8(b.ckpt_gate, "ckpt_gate", rows, hidden, dev), _act8(b.ckpt_up, "ckpt_up", rows, hidden, dev),
+        *_row_major(b.w_gate, "w_gate", hidden, cols, dev, bf16), *_row_major(b.w_up, "w_up", hidden, cols, dev, bf16),
+        *_row_major(b.h, "h", rows, cols, dev, bf16), _act8(b.ckpt_h, "ckpt_h", rows, cols, dev),
+        *_vector(b.col_scale, "col_scale", cols, dev), *wide(b.dgate, "dgate"), *wide(b.dup, "dup"),
+        *_row_major(b.dh, "dh", rows, cols, dev, bf16), *_row_major(b.dw_gate, "dw_gate", hidden, cols, dev),
+        *_row_major(b.dw_up, "dw_up", hidden, cols, dev), _act8(b.ckpt_a, "ckpt_a", rows, hidden, dev),
+        _one_format(b.ckpt_gate, b.ckpt_up, b.ckpt_h, b.ckpt_a), b.act, flags, 0)
+    _check(lib().zero_block_ffn_grad(args, wsp, wsb, _stream_of(stream, dev)), "zero_block_ffn_grad")
+
+
+def _one_format(*checkpoints: Optional[Act8]) -> int:
+    formats = {int(c.format) for c in checkpoints if c is not None}
+    if len(formats) > 1:
+        raise ValueError("the checkpoints have different formats")
+    return formats.pop() if formats else 0
 
 
 def zero_workspace_forget(ws: torch.Tensor) -> None:

@@ -12,7 +12,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 # compiled side by side: each has its own kernels (no device code is shared between objects)
 SOURCES = [os.path.join(CSRC, f) for f in ("zero_kernels.hip", "zero_api.cpp", "zero_act8.hip", "zero_wgrad.hip",
-                                            "zero_block_norm.hip", "zero_block_api.cpp")]
+                                            "zero_block_norm.hip", "zero_layer_norm.hip", "zero_ffn.hip",
+                                            "zero_ffn_act.hip", "zero_block_api.cpp")]
 # host-only C++ (the optimizer half of the CPU-offloaded step), built by the
 # host compiler into an object that the library links
 HOST_SOURCES = [os.path.join(CSRC, "zero_host_adamw.cpp")]

@@ -1,7 +1,7 @@
 // zero_block.h -- host types and launch wrappers of the calls around a
 // training block (8-bit activation checkpoints, the weight gradient taken
-// from one, the norms with gate and residual scale). Not part of the public
-// C ABI.
+// from one, the norms with gate and residual scale, the layer norm, the gated
+// feed-forward block). Not part of the public C ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -126,5 +126,96 @@ struct NormGradArgs {
     float* row_sums;  // [rows][2] with strips
 };
 hipError_t launch_block_norm_grad(const NormGradArgs& a, hipStream_t s);
+
+struct LayerNormArgs {
+    int64_t rows;
+    int64_t unit_rows;  // rows that a workgroup (or wave) takes, set at the launch
+    int32_t cols;
+    float eps;
+    int32_t stream;  // read x and y past the caches, set at the launch
+    Rows x, y, w, b, x_out, h;
+    float* mean;
+    float* rstd;
+    uint8_t* ckpt_xn;
+    uint8_t* ckpt_h;
+    int format;
+};
+hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s);
+
+// The rows of the backward pass: `units` of unit_rows rows, each of which a
+// workgroup (or wave) sums over; a second launch joins their sums.
+struct LayerNormGradPlan {
+    int64_t unit_rows;
+    int64_t units;
+    bool strips;   // rows too wide for one workgroup
+    size_t bytes;  // workspace: two fp32 rows of cols per unit, and for rows in strips two fp32 values per row
+};
+LayerNormGradPlan layer_norm_grad_plan(int64_t rows, int64_t cols);
+
+struct LayerNormGradArgs {
+    int64_t rows;
+    int32_t cols;
+    Rows dh, dx_out, w, x_out, dx, dy, dw, db;
+    const uint8_t* ckpt_xn;
+    const float* mean;
+    const float* rstd;
+    int format;
+    int accumulate;
+    int stream;  // write dx and dy past the caches, set at the launch
+    LayerNormGradPlan plan;
+    float* sum_w;  // [units][cols]: sums of dh * xn
+    float* sum_b;  // [units][cols]: sums of dh
+    float* row_means;  // [rows][2] with strips
+};
+hipError_t launch_layer_norm_grad(const LayerNormGradArgs& a, hipStream_t s);
+
+// The three products of the gated feed-forward block.
+enum FfnKind {
+    kFfnForward,  // [gate | up] = h [w_gate | w_up]^T, with the activation
+    kFfnInput,    // dh = dgate w_gate + dup w_up
+    kFfnWeight,   // dw_gate = dgate^T h and dw_up = dup^T h
+};
+
+// As WgradPlan: tiles of the output, the first `whole` of them summed by one
+// workgroup each, the others over `split` ranges of the summed index.
+struct FfnPlan {
+    int tile;
+    int64_t whole;
+    int split;
+    int64_t chunk;  // steps of a range (the last may have fewer)
+    size_t bytes;   // workspace
+};
+FfnPlan ffn_plan(FfnKind kind, int64_t rows, int64_t cols, int64_t hidden);
+
+struct FfnArgs {
+    int64_t rows, cols, hidden;
+    const uint16_t* h;
+    int64_t ld_h;
+    const uint16_t* w[2];  // w_gate, w_up
+    int64_t ld_w[2];
+    const uint16_t* d[2];  // dgate, dup
+    int64_t ld_d[2];
+    Rows out[2];           // gate and up, or dh, or dw_gate and dw_up; p null: not wanted
+    Rows a;
+    uint8_t* ckpt[2];      // of gate and up, or null
+    int format;
+    int act;
+    int accumulate;
+    int64_t chunk;  // from the plan
+    int split;
+    float* part;
+};
+hipError_t launch_ffn(FfnKind kind, const FfnArgs& a, const FfnPlan& plan, hipStream_t s);
+
+// dgate, dup and a in 8 bits from da and the saved gate and up.
+struct FfnActArgs {
+    int64_t rows, hidden;
+    Rows da, saved[2], d[2];
+    const uint8_t* ckpt[2];  // null: from saved
+    uint8_t* ckpt_a;
+    int format;
+    int act;
+};
+hipError_t launch_ffn_act_grad(const FfnActArgs& a, hipStream_t s);
 
 }  // namespace zero
