@@ -445,9 +445,11 @@ int zero_block_ffn_grad(const zero_block_ffn_grad_args* g, void* ws, size_t ws_b
     if ((coded || g->ckpt_h != nullptr || g->ckpt_a != nullptr) && !format_ok(g->format)) return ZERO_ERR_INVALID_ARGUMENT;
     if (coded != (g->ckpt_up != nullptr)) return ZERO_ERR_INVALID_ARGUMENT;
     const bool weights = given(g->dw_gate) || given(g->dw_up);
-    if (!weights && (given(g->h) || g->ckpt_h != nullptr || given(g->col_scale))) return ZERO_ERR_INVALID_ARGUMENT;
-    if (given(g->col_scale) && g->ckpt_h == nullptr) return ZERO_ERR_INVALID_ARGUMENT;
-    if (!given(g->dh) && (given(g->w_gate) || given(g->w_up))) return ZERO_ERR_INVALID_ARGUMENT;
+    if (g->rows > 0 && g->hidden > 0 && g->cols > 0) {  // an empty operand may have no address
+        if (!weights && (given(g->h) || g->ckpt_h != nullptr || given(g->col_scale))) return ZERO_ERR_INVALID_ARGUMENT;
+        if (given(g->col_scale) && g->ckpt_h == nullptr) return ZERO_ERR_INVALID_ARGUMENT;
+        if (!given(g->dh) && (given(g->w_gate) || given(g->w_up))) return ZERO_ERR_INVALID_ARGUMENT;
+    }
     const int32_t grad_type = accumulate ? ZERO_F32 : 0;
     if (!optional_ok(g->dw_gate, g->cols, grad_type) || !optional_ok(g->dw_up, g->cols, grad_type) ||
         !optional_ok(g->col_scale, g->cols, 0, true) || !optional_ok(g->dh, g->cols, ZERO_BF16))

@@ -42,7 +42,7 @@ __device__ __forceinline__ Terms terms(int act, float g)
     float z = g, dz = 1.0f;  // act(g) = g logistic(z)
     if (act == ZERO_FFN_GELU_TANH) {
         z = 1.59576912f * fmaf(0.044715f * g * g, g, g);
-        dz = fmaf(0.21406f * g, g, 1.59576912f);
+        dz = fmaf(0.214064449f * g, g, 1.59576912f);
     }
     const float e = __builtin_amdgcn_exp2f(z * -1.44269504f), p = __builtin_amdgcn_rcpf(1.0f + e), q = e * p;
     const float steep = g * dz * q;

@@ -28,7 +28,8 @@ def act64(act, g):
 
 def nearest_bf16(x):
     """float64 values rounded to bf16 once (with its subnormals), as float64."""
-    step = torch.ldexp(torch.ones_like(x), (torch.frexp(x)[1] - 8).clamp(min=-133))
+    e = (torch.frexp(x)[1].to(torch.int64) - 8).clamp(min=-133)
+    step = ((e + 1023) << 52).view(torch.float64)
     r = torch.round(x / step) * step
     return torch.where(torch.isfinite(x), r, x)
 

@@ -181,7 +181,8 @@ def check_backward(b, place, gate, up, x, old, where=""):
     rows, hidden = gate.shape
     for k in ("dgate", "dup"):
         # 64-bit formulas differ by a few 2^-52, which does not reach a bf16 border
-        assert torch.equal(getattr(b, k).double(), nearest_bf16(ref[k][0])), (where, k)
+        wrong = int((getattr(b, k).double() != nearest_bf16(ref[k][0])).sum())
+        assert wrong == 0, (where, k, wrong)
     if b.dh is not None:
         assert_within(b.dh, *ref["dh"], (2 * hidden + 64) * U, (where, "dh"))
     for k, o in old.items():
@@ -218,12 +219,12 @@ def test_backward_operands(dh, dw, inp, scale):
 
 def test_backward_of_empty_sizes():
     for acc in (True, False):
-        b = backward(0, 24, 40, accumulate=acc)[0]
+        b = backward(0, 24, 40, accumulate=acc, saved="raw")[0]
         if not acc:
             assert float(b.dw_gate.abs().max()) == float(b.dw_up.abs().max()) == 0.0
     b = backward(5, 24, 0, saved="raw")[0]
     assert float(b.dh.abs().max()) == 0.0
-    backward(5, 0, 40)
+    backward(5, 0, 40, saved="raw")
 
 
 @pytest.mark.parametrize("act", ACTS)
