@@ -176,16 +176,9 @@ enum FfnKind {
     kFfnWeight,   // dw_gate = dgate^T h and dw_up = dup^T h
 };
 
-// As WgradPlan: tiles of the output, the first `whole` of them summed by one
-// workgroup each, the others over `split` ranges of the summed index.
-struct FfnPlan {
-    int tile;
-    int64_t whole;
-    int split;
-    int64_t chunk;  // steps of a range (the last may have fewer)
-    size_t bytes;   // workspace
-};
-FfnPlan ffn_plan(FfnKind kind, int64_t rows, int64_t cols, int64_t hidden);
+// Workspace of a product: the parts of tiles that are split over the summed
+// index, whatever the operands' alignment.
+size_t ffn_workspace_bytes(FfnKind kind, int64_t rows, int64_t cols, int64_t hidden);
 
 struct FfnArgs {
     int64_t rows, cols, hidden;
@@ -201,11 +194,13 @@ struct FfnArgs {
     int format;
     int act;
     int accumulate;
-    int64_t chunk;  // from the plan
-    int split;
     float* part;
+    // set at the launch
+    int plain;      // whole steps of unaligned operands are read at 32-bit offsets
+    int64_t chunk;  // steps of a range of a split tile
+    int split;
 };
-hipError_t launch_ffn(FfnKind kind, const FfnArgs& a, const FfnPlan& plan, hipStream_t s);
+hipError_t launch_ffn(FfnKind kind, const FfnArgs& a, hipStream_t s);
 
 // dgate, dup and a in 8 bits from da and the saved gate and up.
 struct FfnActArgs {

@@ -93,7 +93,7 @@ bool any_same(P... p)
 // The largest of the workspaces of a feed-forward block's products, which run one after the other.
 size_t ffn_grad_bytes(int64_t rows, int64_t cols, int64_t hidden)
 {
-    const size_t input = ffn_plan(kFfnInput, rows, cols, hidden).bytes, weight = ffn_plan(kFfnWeight, rows, cols, hidden).bytes;
+    const size_t input = ffn_workspace_bytes(kFfnInput, rows, cols, hidden), weight = ffn_workspace_bytes(kFfnWeight, rows, cols, hidden);
     const size_t coded = wgrad_plan(rows, hidden, cols).bytes;
     const size_t most = input > weight ? input : weight;
     return most > coded ? most : coded;
@@ -390,7 +390,7 @@ int zero_layer_norm_grad(const zero_layer_norm_grad_args* g, void* ws, size_t ws
 
 size_t zero_block_ffn_workspace_bytes(int64_t rows, int64_t cols, int64_t hidden)
 {
-    return ffn_sizes_ok(rows, cols, hidden) ? ffn_plan(kFfnForward, rows, cols, hidden).bytes : 0;
+    return ffn_sizes_ok(rows, cols, hidden) ? ffn_workspace_bytes(kFfnForward, rows, cols, hidden) : 0;
 }
 
 int zero_block_ffn(const zero_block_ffn_args* g, void* ws, size_t ws_bytes, hipStream_t stream)
@@ -404,11 +404,11 @@ int zero_block_ffn(const zero_block_ffn_args* g, void* ws, size_t ws_bytes, hipS
         return ZERO_ERR_INVALID_ARGUMENT;
     if (!aligned(g->ckpt_gate, kPtrAlign) || !aligned(g->ckpt_up, kPtrAlign)) return ZERO_ERR_INVALID_ARGUMENT;
     if (any_same(g->a.data, g->gate.data, g->up.data, g->ckpt_gate, g->ckpt_up)) return ZERO_ERR_INVALID_ARGUMENT;
-    const FfnPlan plan = ffn_plan(kFfnForward, g->rows, g->cols, g->hidden);
-    if (plan.bytes > 0) {
+    const size_t bytes = ffn_workspace_bytes(kFfnForward, g->rows, g->cols, g->hidden);
+    if (bytes > 0) {
         if (!buffer_ok(ws)) return ZERO_ERR_INVALID_ARGUMENT;
-        if (ws_bytes < plan.bytes) return ZERO_ERR_WORKSPACE_TOO_SMALL;
-        forget_plans(ws, plan.bytes);
+        if (ws_bytes < bytes) return ZERO_ERR_WORKSPACE_TOO_SMALL;
+        forget_plans(ws, bytes);
     }
     FfnArgs a{};
     a.rows = g->rows;
@@ -428,7 +428,7 @@ int zero_block_ffn(const zero_block_ffn_args* g, void* ws, size_t ws_bytes, hipS
     a.format = g->format;
     a.act = g->act;
     a.part = static_cast<float*>(ws);
-    return hip_status(launch_ffn(kFfnForward, a, plan, stream));
+    return hip_status(launch_ffn(kFfnForward, a, stream));
 }
 
 size_t zero_block_ffn_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t hidden)
@@ -504,7 +504,7 @@ int zero_block_ffn_grad(const zero_block_ffn_grad_args* g, void* ws, size_t ws_b
         a.ld_w[0] = g->w_gate.ld;
         a.ld_w[1] = g->w_up.ld;
         a.out[0] = view(g->dh);
-        const hipError_t e = launch_ffn(kFfnInput, a, ffn_plan(kFfnInput, g->rows, g->cols, g->hidden), stream);
+        const hipError_t e = launch_ffn(kFfnInput, a, stream);
         if (e != hipSuccess) return ZERO_ERR_HIP;
     }
     if (!weights || g->hidden == 0 || g->cols == 0 || (g->rows == 0 && accumulate)) return ZERO_OK;
@@ -513,7 +513,7 @@ int zero_block_ffn_grad(const zero_block_ffn_grad_args* g, void* ws, size_t ws_b
         a.ld_h = g->h.ld;
         a.out[0] = view(g->dw_gate);
         a.out[1] = view(g->dw_up);
-        return hip_status(launch_ffn(kFfnWeight, a, ffn_plan(kFfnWeight, g->rows, g->cols, g->hidden), stream));
+        return hip_status(launch_ffn(kFfnWeight, a, stream));
     }
     for (const bool up : {false, true}) {
         const zero_rows& dw = up ? g->dw_up : g->dw_gate;

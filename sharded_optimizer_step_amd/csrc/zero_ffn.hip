@@ -45,6 +45,7 @@ struct Tile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, SLOTS = SLOTS_;
     static constexpr int NT = 64 * WM * WN;
     static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 pieces of a wave
+    static constexpr int kWavesASimd = NT * SLOTS > 256 ? NT * SLOTS / 256 : 1;
 };
 
 // A tile of SIZE rows or columns of a factor and BK elements of the summed
@@ -73,25 +74,27 @@ struct Factor {
     }
 };
 
+// The elements from `shift` on, and zeros.
+__device__ __forceinline__ u32x4 shift_unit(u32x4 v, int shift)
+{
+    uint64_t lo = v.x | static_cast<uint64_t>(v.y) << 32, hi = v.z | static_cast<uint64_t>(v.w) << 32;
+    if (shift >= 4) {
+        lo = hi >> (16 * (shift - 4));
+        hi = 0;
+    } else if (shift > 0) {
+        lo = lo >> (16 * shift) | hi << (64 - 16 * shift);
+        hi >>= 16 * shift;
+    }
+    return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+}
+
 // Elements col .. col + 7 of a row of `limit` elements, zeros beyond it.
 __device__ __forceinline__ u32x4 load_unit(const uint16_t* row, int64_t col, int64_t limit)
 {
     const int64_t left = limit - col;
     if (left >= 8) return ld16_a2(row + col);
     if (left <= 0) return u32x4{};
-    if (limit >= 8) {  // the last 8 of the row, moved into place
-        const u32x4 v = ld16_a2(row + limit - 8);
-        const int shift = static_cast<int>(8 - left);
-        uint64_t lo = v.x | static_cast<uint64_t>(v.y) << 32, hi = v.z | static_cast<uint64_t>(v.w) << 32;
-        if (shift >= 4) {
-            lo = hi >> (16 * (shift - 4));
-            hi = 0;
-        } else {
-            lo = lo >> (16 * shift) | hi << (64 - 16 * shift);
-            hi >>= 16 * shift;
-        }
-        return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
-    }
+    if (limit >= 8) return shift_unit(ld16_a2(row + limit - 8), static_cast<int>(8 - left));
     u32x4 v{};
 #pragma unroll
     for (int i = 0; i < 7; ++i)
@@ -193,7 +196,7 @@ struct Shape {
 };
 
 template <class T, FfnKind KIND, bool FAST>
-__global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void ffn_kernel(FfnArgs a, int tiles_m, int tiles_n, int whole)
+__global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, int tiles_m, int tiles_n, int whole)
 {
     using S = Shape<T, KIND>;
     constexpr bool kAlongA = KIND != kFfnWeight, kAlongB = KIND == kFfnForward;
@@ -230,25 +233,29 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void ffn_kernel(FfnA
     const int row_b = tid / B::kUnits, unit_b = B::place(row_b, tid % B::kUnits);
     // forward the second half of B's rows are those of up
     constexpr int kHalfB = KIND == kFfnForward ? B::kVecs / 2 : B::kVecs;
+    // Rows beyond the last one are read as the last one, columns as the last
+    // eight (which is where a unit that ends beyond them lies, moved into place
+    // by `shift` elements): products of what is beyond are not stored. Offsets
+    // are from eight elements before a tile, so that none is negative.
     uint32_t off_a[A::kVecs], off_b[B::kVecs];
-    if constexpr (FAST) {
-        // Rows and columns beyond the last one are read as the last one: their products are not stored.
 #pragma unroll
-        for (int i = 0; i < A::kVecs; ++i) {
-            const int64_t ld = KIND == kFfnForward ? a.ld_h : a.ld_d[0];
-            const int64_t row = kAlongA ? min(static_cast<int64_t>(row_a + i * A::kStep), m_end - 1 - m0) : row_a + i * A::kStep;
-            const int64_t col = kAlongA ? unit_a * 8 : min(static_cast<int64_t>(unit_a * 8), m_end - 8 - m0);
-            off_a[i] = static_cast<uint32_t>((row * ld + col) * 2);
-        }
-#pragma unroll
-        for (int i = 0; i < B::kVecs; ++i) {
-            const int64_t ld = KIND == kFfnWeight ? a.ld_h : a.ld_w[0];
-            const int r = row_b + i % kHalfB * B::kStep;
-            const int64_t row = kAlongB ? min(static_cast<int64_t>(r), n_end - 1 - n0) : r;
-            const int64_t col = kAlongB ? unit_b * 8 : min(static_cast<int64_t>(unit_b * 8), n_end - 8 - n0);
-            off_b[i] = static_cast<uint32_t>((row * ld + col) * 2);
-        }
+    for (int i = 0; i < A::kVecs; ++i) {
+        const int64_t ld = KIND == kFfnForward ? a.ld_h : a.ld_d[which];
+        const int64_t row = kAlongA ? min(static_cast<int64_t>(row_a + i * A::kStep), m_end - 1 - m0) : row_a + i * A::kStep;
+        const int64_t col = kAlongA ? unit_a * 8 : min(static_cast<int64_t>(unit_a * 8), m_end - 8 - m0);
+        off_a[i] = static_cast<uint32_t>((row * ld + col + 8) * 2);
     }
+#pragma unroll
+    for (int i = 0; i < B::kVecs; ++i) {
+        const int64_t ld = KIND == kFfnWeight ? a.ld_h : a.ld_w[KIND == kFfnForward && i >= kHalfB ? 1 : 0];
+        const int r = row_b + i % kHalfB * B::kStep;
+        const int64_t row = kAlongB ? min(static_cast<int64_t>(r), n_end - 1 - n0) : r;
+        const int64_t col = kAlongB ? unit_b * 8 : min(static_cast<int64_t>(unit_b * 8), n_end - 8 - n0);
+        off_b[i] = static_cast<uint32_t>((row * ld + col + 8) * 2);
+    }
+    const int over_a = static_cast<int>(unit_a * 8 - (m_end - 8 - m0)), over_b = static_cast<int>(unit_b * 8 - (n_end - 8 - n0));
+    const int shift_a = !FAST && !kAlongA && over_a > 0 && over_a < 8 ? over_a : 0;
+    const int shift_b = !FAST && !kAlongB && over_b > 0 && over_b < 8 ? over_b : 0;
     struct Step {
         const uint16_t *a, *b0, *b1;
         int64_t left;  // summed elements from this step on
@@ -274,47 +281,71 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void ffn_kernel(FfnA
     // A step's tiles straight to LDS. (In the last one, elements beyond the sum are read from beyond the buffer: zeros.)
     const auto send = [&](int64_t s, char* sa, char* sb) {
         const Step t = step_at(s);
-        const __amdgpu_buffer_rsrc_t ra = buffer_at(t.a), rb0 = buffer_at(t.b0), rb1 = buffer_at(t.b1);
-        const bool full = t.left >= BK;
+        const __amdgpu_buffer_rsrc_t ra = buffer_at(t.a - 8), rb0 = buffer_at(t.b0 - 8), rb1 = buffer_at(t.b1 - 8);
+        const auto load = [&](int i, bool b, uint32_t off) {
+            char* to = (b ? sb : sa) + (i * T::NT + wave * 64) * 16;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(!b ? ra : i < kHalfB ? rb0 : rb1, (ZERO_L void*)to, 16, off, 0, 0, 0);
+        };
+        if (t.left >= BK) {
 #pragma unroll
-        for (int i = 0; i < A::kVecs; ++i) {
-            uint32_t off = off_a[i];
-            if (!full && (kAlongA ? unit_a * 8 : row_a + i * A::kStep) >= t.left) off = kBeyond;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (ZERO_L void*)(sa + (i * T::NT + wave * 64) * 16), 16, off, 0, 0, 0);
-        }
+            for (int i = 0; i < A::kVecs; ++i) load(i, false, off_a[i]);
 #pragma unroll
-        for (int i = 0; i < B::kVecs; ++i) {
-            uint32_t off = off_b[i];
-            if (!full && (kAlongB ? unit_b * 8 : row_b + i * B::kStep) >= t.left) off = kBeyond;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(i < kHalfB ? rb0 : rb1, (ZERO_L void*)(sb + (i * T::NT + wave * 64) * 16), 16, off, 0, 0, 0);
+            for (int i = 0; i < B::kVecs; ++i) load(i, true, off_b[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < A::kVecs; ++i) load(i, false, (kAlongA ? unit_a * 8 : row_a + i * A::kStep) >= t.left ? kBeyond : off_a[i]);
+#pragma unroll
+            for (int i = 0; i < B::kVecs; ++i) load(i, true, (kAlongB ? unit_b * 8 : row_b + i * B::kStep) >= t.left ? kBeyond : off_b[i]);
         }
     };
-    // Or through registers, for operands whose rows do not all lie on 16 bytes.
+    // Or through registers, where the rows of an operand do not all lie on 16 bytes.
     u32x4 va[A::kVecs], vb[B::kVecs];
+    // Steps that are whole go with their loads in flight over a step.
+    const auto in_flight = [&](int64_t left) { return a.plain != 0 && left >= BK; };
     const auto fetch = [&](int64_t s) {
         const Step t = step_at(s);
-        const int seg = KIND == kFfnInput && s >= seg_steps ? 1 : 0;
+        if (!in_flight(t.left)) return;
+        const char *pa = reinterpret_cast<const char*>(t.a - 8), *pb0 = reinterpret_cast<const char*>(t.b0 - 8), *pb1 = reinterpret_cast<const char*>(t.b1 - 8);
 #pragma unroll
+        for (int i = 0; i < A::kVecs; ++i) va[i] = ld16_a2(pa + off_a[i]);
+#pragma unroll
+        for (int i = 0; i < B::kVecs; ++i) vb[i] = ld16_a2((i < kHalfB ? pb0 : pb1) + off_b[i]);
+    };
+    // What fetch(s) read, to its tiles; or the step's units one after the other, each no further than its row goes.
+    const auto stage = [&](int64_t s, char* sa, char* sb) {
+        const Step t = step_at(s);
+        if (in_flight(t.left)) {
+            if (!kAlongA && m0 + T::BM > m_end) {
+#pragma unroll
+                for (int i = 0; i < A::kVecs; ++i) va[i] = shift_unit(va[i], shift_a);
+            }
+            if (!kAlongB && n0 + S::kCols > n_end) {
+#pragma unroll
+                for (int i = 0; i < B::kVecs; ++i) vb[i] = shift_unit(vb[i], shift_b);
+            }
+#pragma unroll
+            for (int i = 0; i < A::kVecs; ++i) *reinterpret_cast<u32x4*>(sa + (i * T::NT + tid) * 16) = va[i];
+#pragma unroll
+            for (int i = 0; i < B::kVecs; ++i) *reinterpret_cast<u32x4*>(sb + (i * T::NT + tid) * 16) = vb[i];
+            return;
+        }
+        const int seg = KIND == kFfnInput && s >= seg_steps ? 1 : 0;
+#pragma unroll 1
         for (int i = 0; i < A::kVecs; ++i) {
             const int row = row_a + i * A::kStep;
             const int64_t ld = KIND == kFfnForward ? a.ld_h : a.ld_d[KIND == kFfnInput ? seg : which];
-            va[i] = u32x4{};
-            if (row < (kAlongA ? m_end - m0 : t.left)) va[i] = load_unit(t.a + row * ld, unit_a * 8, kAlongA ? t.left : m_end - m0);
+            u32x4 v{};
+            if (row < (kAlongA ? m_end - m0 : t.left)) v = load_unit(t.a + row * ld, unit_a * 8, kAlongA ? t.left : m_end - m0);
+            *reinterpret_cast<u32x4*>(sa + (i * T::NT + tid) * 16) = v;
         }
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < B::kVecs; ++i) {
-            const int row = row_b + i % kHalfB * B::kStep;
-            const int64_t ld = KIND == kFfnWeight ? a.ld_h : a.ld_w[KIND == kFfnInput ? seg : i < kHalfB ? 0 : 1];
-            vb[i] = u32x4{};
-            if (row < (kAlongB ? n_end - n0 : t.left))
-                vb[i] = load_unit((i < kHalfB ? t.b0 : t.b1) + row * ld, unit_b * 8, kAlongB ? t.left : n_end - n0);
+            const int up = i < kHalfB ? 0 : 1, row = row_b + (i - up * kHalfB) * B::kStep;
+            const int64_t ld = KIND == kFfnWeight ? a.ld_h : a.ld_w[KIND == kFfnInput ? seg : up];
+            u32x4 v{};
+            if (row < (kAlongB ? n_end - n0 : t.left)) v = load_unit((up ? t.b1 : t.b0) + row * ld, unit_b * 8, kAlongB ? t.left : n_end - n0);
+            *reinterpret_cast<u32x4*>(sb + (i * T::NT + tid) * 16) = v;
         }
-    };
-    const auto stage = [&](char* sa, char* sb) {
-#pragma unroll
-        for (int i = 0; i < A::kVecs; ++i) *reinterpret_cast<u32x4*>(sa + (i * T::NT + tid) * 16) = va[i];
-#pragma unroll
-        for (int i = 0; i < B::kVecs; ++i) *reinterpret_cast<u32x4*>(sb + (i * T::NT + tid) * 16) = vb[i];
     };
 
     // Where this lane reads. The four groups of 16 lanes take summed elements 8 g
@@ -322,74 +353,102 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void ffn_kernel(FfnA
     // across, the 16 lanes of a group read 4 elements' rows, 4 columns a lane, and
     // get a column of all 4 each.
     const int wm = wave / T::WN, wn = wave % T::WN, group = lane / 16, in_group = lane % 16;
+    // In both layouts the lane's part of the address and the piece's meet in
+    // different bits, or by exclusive or in the bits that are permuted.
+    const int across_row = 8 * group + in_group / 4;
+    uint32_t at_a, at_b;  // of piece 0, summed element 0
+    if constexpr (kAlongA) at_a = (wm * (T::BM / T::WM) + in_group) * A::kRowBytes + A::place(in_group, group) * 16;
+    else at_a = across_row * A::kRowBytes + A::place(across_row, wm * (T::BM / T::WM) / 8) * 16 + in_group % 4 * 8;
+    constexpr int kColsB = S::kCols / T::WN;  // forward a wave's first pieces are of gate, the others of as many columns of up
+    if constexpr (kAlongB) at_b = (wn * kColsB + in_group) * B::kRowBytes + B::place(in_group, group) * 16;
+    else at_b = across_row * B::kRowBytes + B::place(across_row, wn * kColsB / 8) * 16 + in_group % 4 * 8;
     const auto piece_a = [&](const char* sa, int i, int k) {
-        if constexpr (kAlongA) return sa + (wm * (T::BM / T::WM) + 16 * i + in_group) * A::kRowBytes + A::place(in_group, k / 8 + group) * 16;
-        else {
-            const int row = 8 * group + in_group / 4, col = wm * (T::BM / T::WM) + 16 * i;
-            return sa + (k + row) * A::kRowBytes + A::place(row, col / 8) * 16 + in_group % 4 * 8;
-        }
+        if constexpr (kAlongA) return sa + ((at_a ^ k * 2) + 16 * i * A::kRowBytes);
+        else return sa + ((at_a ^ i * 32) + k * A::kRowBytes);
     };
-    // Forward a wave's first pieces are of gate, the others of up.
     const auto piece_b = [&](const char* sb, int j, int k) {
-        const int col = KIND == kFfnForward ? (j < T::TN / 2 ? 0 : T::BN / 2 - T::TN * 8) + wn * (T::TN * 8) + 16 * j : wn * (T::BN / T::WN) + 16 * j;
-        if constexpr (kAlongB) return sb + (col + in_group) * B::kRowBytes + B::place(in_group, k / 8 + group) * 16;
-        else {
-            const int row = 8 * group + in_group / 4;
-            return sb + (k + row) * B::kRowBytes + B::place(row, col / 8) * 16 + in_group % 4 * 8;
-        }
+        if constexpr (kAlongB) {
+            const int row = 16 * j + (KIND == kFfnForward && j >= T::TN / 2 ? T::BN / 2 - T::TN * 8 : 0);
+            return sb + ((at_b ^ k * 2) + row * B::kRowBytes);
+        } else return sb + ((at_b ^ j * 32) + k * B::kRowBytes);
     };
     f32x4 acc[T::TN][T::TM];
 #pragma unroll
     for (int j = 0; j < T::TN; ++j)
 #pragma unroll
         for (int i = 0; i < T::TM; ++i) acc[j][i] = f32x4{};
-    const auto multiply = [&](const char* sa, const char* sb) {
-#pragma unroll
-        for (int k = 0; k < BK; k += 32) {
-            bf16x8 fa[T::TM], fb[T::TN];
-#pragma unroll
-            for (int j = 0; j < T::TN; ++j) fb[j] = read_piece<kAlongB, B::kRowBytes>(piece_b(sb, j, k));
-#pragma unroll
-            for (int i = 0; i < T::TM; ++i) fa[i] = read_piece<kAlongA, A::kRowBytes>(piece_a(sa, i, k));
-#pragma unroll
-            for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-                for (int j = 0; j < T::TN; ++j)
-                    acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[j][i], 0, 0, 0);
-        }
+    struct Half {  // of a step: the pieces of 32 summed elements
+        bf16x8 a[T::TM], b[T::TN];
     };
-    // All of this step's loads to LDS have arrived and all of its reads from it
-    // are done, in every wave.
+    const auto read = [&](Half& h, const char* sa, const char* sb, int k) {
+        // (kept from the compiler, which would hold the address of every piece in a register)
+        asm volatile("" : "+v"(at_a), "+v"(at_b));
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) h.b[j] = read_piece<kAlongB, B::kRowBytes>(piece_b(sb, j, k));
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i) h.a[i] = read_piece<kAlongA, A::kRowBytes>(piece_a(sa, i, k));
+    };
+    const auto multiply = [&](const Half& h) {
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < T::TN; ++j) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h.b[j], h.a[i], acc[j][i], 0, 0, 0);
+    };
+    // This wave's loads to LDS have arrived and its reads and writes of it are done, and so are all waves'.
     const auto meet = [&] {
+        __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
-    // One step from its tiles while the next one's go to the other two, whose
-    // last reads were before the last barrier.
+    // A step, of which the first half is in registers already. Its second half
+    // is read while the first is multiplied. With that the step's tiles are free
+    // for the step after the next, whose loads are then in flight for a step, and
+    // the next one's have arrived: its first half is read while the second half is
+    // multiplied. So the waves meet once a step, with products on both sides.
+    Half h0, h1;
     const auto step = [&](int64_t s, char* sa, char* sb, char* next_a, char* next_b) {
+        read(h1, sa, sb, 32);
+        multiply(h0);
         if constexpr (FAST) {
-            if (s + 1 < end) send(s + 1, next_a, next_b);
-            multiply(sa, sb);
+            meet();
+            if (s + 2 < end) send(s + 2, sa, sb);
         } else {
-            if (s + 1 < end) fetch(s + 1);
-            multiply(sa, sb);
-            if (s + 1 < end) stage(next_a, next_b);
+            // (only the reads and writes of LDS: the loads to registers go on)
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            if (s + 2 < end) stage(s + 2, sa, sb);
+            if (s + 3 < end) fetch(s + 3);
         }
-        meet();
+        if (s + 1 < end) read(h0, next_a, next_b, 0);
+        multiply(h1);
+        __builtin_amdgcn_sched_barrier(0);
     };
     if (begin < end) {
-        if constexpr (FAST) send(begin, sa0, sb0);
-        else {
+        if constexpr (FAST) {
+            send(begin, sa0, sb0);
+            if (begin + 1 < end) send(begin + 1, sa1, sb1);
+        } else {
             fetch(begin);
-            stage(sa0, sb0);
+            stage(begin, sa0, sb0);
+            if (begin + 1 < end) {
+                fetch(begin + 1);
+                stage(begin + 1, sa1, sb1);
+            }
+            if (begin + 2 < end) fetch(begin + 2);
         }
         meet();
+        read(h0, sa0, sb0, 0);
     }
     for (int64_t s = begin; s < end; s += 2) {
         step(s, sa0, sb0, sa1, sb1);
         if (s + 1 < end) step(s + 1, sa1, sb1, sa0, sb0);
     }
+    // the last step's tiles are read, in every wave, since its meeting
 
     // B is the first operand, so a lane holds four neighbouring columns of one
     // row of the output. Sixteen rows at a time go through LDS (each wave its own
@@ -399,9 +458,11 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void ffn_kernel(FfnA
     // moving a lane's reads over its writes, which other lanes read; a wave's LDS
     // accesses are in order.
     constexpr int kWide = T::TN * 16, kOut = KIND == kFfnForward ? kWide / 2 : kWide, kLanes = kOut / 8, kPad = kWide + 4;
-    static_assert(T::NT / 256 * 16 * kPad * sizeof(float) <= sizeof(sa0) && T::BN >= T::BM, "each array holds 16 rows of a fourth of the waves");
+    static_assert(KIND != kFfnForward || kOut % kActBlock == 0, "a block of 32 columns lies in one wave");
+    constexpr int kRoom = (T::NT / 64 + 3) / 4 * 16 * kPad * 4;  // of a fourth of the waves
+    static_assert(kRoom <= sizeof(sb0) && (T::NT <= 128 || kRoom <= sizeof(sa0)), "each array holds 16 rows of a fourth of the waves");
     const int quarter = wave % 4;
-    float* out = reinterpret_cast<float*>(quarter == 0 ? sa0 : quarter == 1 ? sa1 : quarter == 2 ? sb0 : sb1) + wave / 4 * 16 * kPad;
+    float* out = reinterpret_cast<float*>(quarter == 0 ? sb0 : quarter == 1 ? sb1 : quarter == 2 ? sa0 : sa1) + wave / 4 * 16 * kPad;
     const int64_t n = n0 + wn * kOut + lane % kLanes * 8;
     const int left = static_cast<int>(min(n_end - n, int64_t{8}));
 #pragma unroll
@@ -420,6 +481,7 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void ffn_kernel(FfnA
                 *reinterpret_cast<f32x4*>(f + c) = *reinterpret_cast<const f32x4*>(from + c);
                 if constexpr (KIND == kFfnForward) *reinterpret_cast<f32x4*>(u + c) = *reinterpret_cast<const f32x4*>(from + kOut + c);
             }
+            if (m >= m_end) continue;
             if (parted) {
                 float* to = a.part + (static_cast<int64_t>(split_tile) * a.split + part) * (T::BM * T::BN) + tile_row * T::BN + wn * kOut + lane % kLanes * 8;
 #pragma unroll
@@ -427,7 +489,7 @@ __global__ __launch_bounds__(T::NT, T::NT / 256 * T::SLOTS) void ffn_kernel(FfnA
                     *(ZERO_G f32x4*)(to + c) = *reinterpret_cast<f32x4*>(f + c);
                     if constexpr (KIND == kFfnForward) *(ZERO_G f32x4*)(to + T::BN / 2 + c) = *reinterpret_cast<f32x4*>(u + c);
                 }
-            } else if (m < m_end) {
+            } else {
                 finish<KIND>(a, which, m, n, left, f, u);
             }
         }
@@ -480,25 +542,52 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(FfnArgs a, int tiles_m, i
     finish<KIND>(a, which, m, n, static_cast<int>(min(S::n(a) - n, int64_t{8})), f, u);
 }
 
-using TileBigF = Tile<256, 256, 4, 2, 1>;  // forward: a wave's columns of gate and of up fill a line each
-using TileBig = Tile<256, 256, 2, 4, 1>;
-using TileMid = Tile<128, 128, 2, 2, 2>;
+// Forward a wave's columns of gate, and as many of up, are 64 or 32, a line of
+// each; otherwise its 128 x 64 sums read the fewest pieces.
+template <FfnKind KIND>
+using Big = Tile<256, 256, KIND == kFfnForward ? 4 : 2, KIND == kFfnForward ? 2 : 4, 1>;
+using Mid = Tile<128, 128, 2, 2, 2>;
+using Small = Tile<64, 128, 2, 2, 3>;
+template <FfnKind KIND>
+using Flat = Tile<32, 128, 1, KIND == kFfnForward ? 2 : 4, 4>;
+using Slow = Tile<128, 128, 2, 2, 2>;  // through registers
 
-bool on_16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * 2) % 16 == 0 && ld <= (int64_t{1} << 22); }
+// Whether 32-bit offsets reach over the 256 rows of a tile, the same ones in
+// both segments, and what runs across the summed index has a whole unit.
+template <FfnKind KIND>
+bool plain(const FfnArgs& a)
+{
+    const auto reach = [](int64_t ld) { return ld <= (int64_t{1} << 22); };
+    const bool h = reach(a.ld_h), d = reach(a.ld_d[0]) && reach(a.ld_d[1]), w = reach(a.ld_w[0]) && reach(a.ld_w[1]);
+    if (KIND == kFfnForward) return h && w;
+    if (KIND == kFfnInput) return d && w && a.ld_d[0] == a.ld_d[1] && a.ld_w[0] == a.ld_w[1] && a.cols >= 8;
+    return d && h && a.hidden >= 8 && a.cols >= 8;
+}
 
-// Whether every 16-byte unit that a product reads lies on 16 bytes and inside
-// its row, and 32-bit offsets reach over a tile.
+// Whether every 16-byte unit that a product reads also lies on 16 bytes and inside its row.
 template <FfnKind KIND>
 bool fast(const FfnArgs& a)
 {
-    const bool h = on_16(a.h, a.ld_h), d = on_16(a.d[0], a.ld_d[0]) && on_16(a.d[1], a.ld_d[1]) && a.ld_d[0] == a.ld_d[1];
-    const bool w = on_16(a.w[0], a.ld_w[0]) && on_16(a.w[1], a.ld_w[1]) && a.ld_w[0] == a.ld_w[1];
-    if (KIND == kFfnForward) return h && w && a.cols % 8 == 0;
-    if (KIND == kFfnInput) return d && w && a.cols % 8 == 0 && a.hidden % 8 == 0;
-    return d && h && a.cols % 8 == 0 && a.hidden % 8 == 0;
+    const auto on_16 = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * 2) % 16 == 0; };
+    const bool h = on_16(a.h, a.ld_h), d = on_16(a.d[0], a.ld_d[0]) && on_16(a.d[1], a.ld_d[1]);
+    const bool w = on_16(a.w[0], a.ld_w[0]) && on_16(a.w[1], a.ld_w[1]);
+    if (!plain<KIND>(a) || a.cols % 8 != 0) return false;
+    if (KIND == kFfnForward) return h && w;
+    return a.hidden % 8 == 0 && d && (KIND == kFfnInput ? w : h);
 }
 
-template <class T, FfnKind KIND>
+// Tiles of the output, the first `whole` of them summed by one workgroup each,
+// the others over `split` ranges of steps, whose sums go to the workspace (a
+// tile's ranges next to each other), and a second launch adds them in order.
+struct FfnPlan {
+    int tile;
+    int64_t whole;
+    int split;
+    int64_t chunk;  // steps of a range (the last may have fewer)
+    size_t bytes;   // workspace
+};
+
+template <class T, FfnKind KIND, bool FAST>
 hipError_t launch_tile(const FfnArgs& a, const FfnPlan& plan, hipStream_t s)
 {
     using S = Shape<T, KIND>;
@@ -506,38 +595,109 @@ hipError_t launch_tile(const FfnArgs& a, const FfnPlan& plan, hipStream_t s)
     const int n = static_cast<int>((S::n(a) + S::kCols - 1) / S::kCols);
     const int whole = static_cast<int>(plan.whole), rest = m * n - whole;
     const unsigned grid = static_cast<unsigned>((whole + 7) / 8 * 8 + (static_cast<int64_t>(rest) * plan.split + 7) / 8 * 8);
-    if (fast<KIND>(a)) ffn_kernel<T, KIND, true><<<grid, T::NT, 0, s>>>(a, m, n, whole);
-    else ffn_kernel<T, KIND, false><<<grid, T::NT, 0, s>>>(a, m, n, whole);
+    ffn_kernel<T, KIND, FAST><<<grid, T::NT, 0, s>>>(a, m, n, whole);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || rest == 0 || plan.split == 1) return e;
-    ffn_join_kernel<T, KIND><<<dim3(T::BM * S::kCols / 8 / 256, static_cast<unsigned>(rest)), 256, 0, s>>>(a, m, n, whole);
+    if (e != hipSuccess || rest == 0) return e;
+    ffn_join_kernel<T, KIND><<<dim3((T::BM * S::kCols / 8 + 255) / 256, static_cast<unsigned>(rest)), 256, 0, s>>>(a, m, n, whole);
     return hipGetLastError();
+}
+
+// A tile shape, the time of a step of one of its workgroups alone on its
+// compute unit, and that of a step of as many as the chip holds at once, us.
+struct Candidate {
+    int tile, bm, bn, slots;
+    double alone, full;
+};
+template <class T>
+constexpr Candidate candidate(int tile, double alone, double full)
+{
+    return Candidate{tile, T::BM, T::BN, T::SLOTS, alone, full};
+}
+enum TileId { kBig, kMid, kSmall, kFlat, kSlow };
+
+FfnPlan plan_for(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t hidden)
+{
+    static const Candidate kTiles[] = {candidate<Flat<kFfnForward>>(kFlat, 0.60, 3.3), candidate<Small>(kSmall, 0.70, 1.3),
+                                       candidate<Mid>(kMid, 0.85, 1.2), candidate<Big<kFfnForward>>(kBig, 1.6, 1.7)};
+    static const Candidate kSlowTile = candidate<Slow>(kSlow, 1.5, 2.0);
+    constexpr double kStart = 4.0, kJoin = 5.0, kBytes = 2e6;  // us a round, us a join, bytes of parts written and read a us
+    constexpr int64_t kMostParts = int64_t{1} << 16;           // tiles of one join (its grid's second size)
+    const int64_t m = kind == kFfnWeight ? hidden : rows, n = kind == kFfnForward ? 2 * hidden : cols;
+    const int64_t k = kind == kFfnForward ? cols : kind == kFfnInput ? hidden : rows;
+    const int64_t all_steps = (k + BK - 1) / BK * (kind == kFfnInput ? 2 : 1);
+    FfnPlan best{};
+    double least = -1.0;
+    const auto consider = [&](const Candidate& c) {
+        const int64_t tiles = (m + c.bm - 1) / c.bm * ((n + c.bn - 1) / c.bn) * (kind == kFfnWeight ? 2 : 1);
+        const int64_t slots = static_cast<int64_t>(c.slots) * kComputeUnits;
+        const auto rounds = [&](int64_t groups, int64_t steps) {
+            const int64_t full = groups / slots, more = groups % slots;
+            const auto step = [&](double fill) { return fill * c.full > c.alone ? fill * c.full : c.alone; };
+            return static_cast<double>(full) * (kStart + static_cast<double>(steps) * step(1.0)) +
+                   (more > 0 ? kStart + static_cast<double>(steps) * step(static_cast<double>(more) / static_cast<double>(slots)) : 0.0);
+        };
+        const double unsplit = rounds(tiles, all_steps);
+        if (least < 0.0 || unsplit < least) {
+            least = unsplit;
+            best = FfnPlan{c.tile, tiles, 1, all_steps, 0};
+        }
+        const int64_t full_rounds = tiles / slots * slots;
+        for (const int64_t whole : {int64_t{0}, full_rounds}) {
+            const int64_t rest = tiles - whole;
+            if (rest == 0 || rest >= kMostParts || (whole == 0 && rest > 2 * slots)) continue;
+            for (const int want : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+                if (all_steps < 2 * want) break;
+                const int64_t steps = (all_steps + want - 1) / want;
+                const int64_t split = (all_steps + steps - 1) / steps;
+                const double bytes = 4.0 * static_cast<double>(rest * split) * c.bm * c.bn;
+                const double us = (whole > 0 ? rounds(whole, all_steps) : 0.0) + rounds(rest * split, steps) + kJoin + bytes / kBytes;
+                if (us < least) {
+                    least = us;
+                    best = FfnPlan{c.tile, whole, static_cast<int>(split), steps, static_cast<size_t>(bytes)};
+                }
+            }
+            if (full_rounds == 0) break;
+        }
+    };
+    if (!aligned) consider(kSlowTile);
+    else
+        for (const Candidate& c : kTiles)
+            if (kind != kFfnWeight || c.bm >= 128) consider(c);
+    return best;
+}
+
+template <FfnKind KIND>
+hipError_t launch_kind(FfnArgs a, hipStream_t s)
+{
+    a.plain = plain<KIND>(a);
+    const bool aligned = fast<KIND>(a);
+    const FfnPlan plan = plan_for(KIND, aligned, a.rows, a.cols, a.hidden);
+    a.chunk = plan.chunk;
+    a.split = plan.split;
+    switch (plan.tile) {
+    case kBig: return launch_tile<Big<KIND>, KIND, true>(a, plan, s);
+    case kMid: return launch_tile<Mid, KIND, true>(a, plan, s);
+    case kSlow: return launch_tile<Slow, KIND, false>(a, plan, s);
+    default: break;
+    }
+    if constexpr (KIND != kFfnWeight) {  // its columns' tiles are 128 or more: their units are permuted by pairs of eight
+        if (plan.tile == kSmall) return launch_tile<Small, KIND, true>(a, plan, s);
+        return launch_tile<Flat<KIND>, KIND, true>(a, plan, s);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-FfnPlan ffn_plan(FfnKind kind, int64_t rows, int64_t cols, int64_t hidden)
+size_t ffn_workspace_bytes(FfnKind kind, int64_t rows, int64_t cols, int64_t hidden)
 {
-    const int64_t m = kind == kFfnWeight ? hidden : rows, n = kind == kFfnForward ? 2 * hidden : cols;
-    const int64_t k = kind == kFfnForward ? cols : kind == kFfnInput ? hidden : rows;
-    const int64_t steps = (k + BK - 1) / BK * (kind == kFfnInput ? 2 : 1);
-    const auto tiles = [&](int64_t bm, int64_t bn) { return (m + bm - 1) / bm * ((n + bn - 1) / bn) * (kind == kFfnWeight ? 2 : 1); };
-    FfnPlan p{};
-    p.tile = tiles(256, 256) >= kComputeUnits ? 0 : 1;
-    p.whole = p.tile == 0 ? tiles(256, 256) : tiles(128, 128);
-    p.split = 1;
-    p.chunk = steps;
-    return p;
+    const size_t aligned = plan_for(kind, true, rows, cols, hidden).bytes, slow = plan_for(kind, false, rows, cols, hidden).bytes;
+    return aligned > slow ? aligned : slow;
 }
 
-hipError_t launch_ffn(FfnKind kind, const FfnArgs& args, const FfnPlan& plan, hipStream_t s)
+hipError_t launch_ffn(FfnKind kind, const FfnArgs& a, hipStream_t s)
 {
-    FfnArgs a = args;
-    a.chunk = plan.chunk;
-    a.split = plan.split;
-    if (kind == kFfnForward) return plan.tile == 0 ? launch_tile<TileBigF, kFfnForward>(a, plan, s) : launch_tile<TileMid, kFfnForward>(a, plan, s);
-    if (kind == kFfnInput) return plan.tile == 0 ? launch_tile<TileBig, kFfnInput>(a, plan, s) : launch_tile<TileMid, kFfnInput>(a, plan, s);
-    return plan.tile == 0 ? launch_tile<TileBig, kFfnWeight>(a, plan, s) : launch_tile<TileMid, kFfnWeight>(a, plan, s);
+    return kind == kFfnForward ? launch_kind<kFfnForward>(a, s) : kind == kFfnInput ? launch_kind<kFfnInput>(a, s) : launch_kind<kFfnWeight>(a, s);
 }
 
 }  // namespace zero
