@@ -8,6 +8,8 @@
 // reads 8 of them at once; where it is the slow one (the weights for dh, both
 // factors of the weight gradients) the tile lies as in memory and the
 // transposing LDS reads turn it.
+#include <type_traits>
+
 #include "zero_act8_device.h"
 
 namespace zero {
@@ -15,10 +17,10 @@ namespace {
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 #define ZERO_L __attribute__((address_space(3)))
 
-constexpr int BK = 64;  // summed elements of a step
+constexpr int BK = 32;  // summed elements of a step
 
 // ------------------------------------------------------------------ activations
 
@@ -39,24 +41,26 @@ __device__ __forceinline__ float activation(int act, float g)
 
 // ------------------------------------------------------------------ tiles in LDS
 
-// BM x BN tile of the output, WM x WN waves, SLOTS workgroups a compute unit.
-template <int BM_, int BN_, int WM_, int WN_, int SLOTS_>
+// BM x BN tile of the output, WM x WN waves, DEPTH steps in LDS, SLOTS
+// workgroups a compute unit.
+template <int BM_, int BN_, int WM_, int WN_, int DEPTH_, int SLOTS_>
 struct Tile {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, SLOTS = SLOTS_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, DEPTH = DEPTH_, SLOTS = SLOTS_;
     static constexpr int NT = 64 * WM * WN;
     static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 pieces of a wave
     static constexpr int kWavesASimd = NT * SLOTS > 256 ? NT * SLOTS / 256 : 1;
 };
 
 // A tile of SIZE rows or columns of a factor and BK elements of the summed
-// index. ALONG: the summed index runs along its rows, of 128 bytes; otherwise
+// index. ALONG: the summed index runs along its rows, of 64 bytes; otherwise
 // across them, of 2 SIZE bytes.
 //
 // Tiles go from memory to LDS without passing through registers, a wave's 64
 // units of 16 bytes one after the other, so they cannot be padded. The units
-// are permuted within their rows instead. ALONG: 16 lanes read the same unit of
-// 16 rows, and two rows are one span of the 64 banks, so unit u of row r lies
-// at u ^ (r / 2 % 8). Across: 32 lanes of a transposing read take 32 bytes, two
+// are permuted within their rows instead. ALONG: four rows are one span of the
+// 64 banks, and a read is served in four parts of 16 lanes, lanes 0 .. 3, 12 ..
+// 15 and 20 .. 27 of 32 or the others: with the rows' units permuted by 0, 2, 3,
+// 1 for each four rows, and so 16 neighbouring lanes too, they lie apart. Across: 32 lanes of a transposing read take 32 bytes, two
 // units, of rows 0 .. 3 and 8 .. 11 of 16 (or the others), whose pairs of units
 // are permuted by eight different numbers.
 template <bool ALONG, int SIZE, int NT>
@@ -65,12 +69,12 @@ struct Factor {
     static constexpr int kUnits = kRowBytes / 16;             // of a row
     static constexpr int kVecs = SIZE * BK * 2 / 16 / NT;     // units a thread loads
     static constexpr int kStep = NT / kUnits;                 // rows from one of them to the next
-    static_assert(NT % kUnits == 0 && kStep % 16 == 0, "a thread's units lie at one place of their rows");
+    static_assert(SIZE * BK * 2 / 16 % NT == 0 && NT % kUnits == 0, "every thread loads as many units, at one place of their rows");
     static_assert(ALONG || SIZE >= 128, "eight pairs of units");
 
     static __device__ __forceinline__ int place(int row, int unit)
     {
-        return ALONG ? unit ^ (row >> 1 & 7) : unit ^ ((row & 3) << 1 | (row >> 3 & 1) << 3);
+        return ALONG ? unit ^ ((row >> 2 ^ row >> 3) & 1) << 1 ^ (row >> 3 & 1) : unit ^ ((row & 3) << 1 | (row >> 3 & 1) << 3);
     }
 };
 
@@ -103,24 +107,53 @@ __device__ __forceinline__ u32x4 load_unit(const uint16_t* row, int64_t col, int
 }
 
 // A raw buffer of 2 GiB from p on; loads from offsets beyond it give zeros.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const uint16_t* p)
+__device__ __forceinline__ i32x4 buffer_at(const uint16_t* p)
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, 0x80000000u, 0x00020000);
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    return i32x4{static_cast<int>(at), static_cast<int>(at >> 32 & 0xFFFF), static_cast<int>(0x80000000u), 0x00020000};
 }
 constexpr uint32_t kBeyond = 0xFFFFFF00u;
+
+// 16 bytes a lane from `offset` of a buffer to LDS, a wave's 64 units one after
+// the other from `to` on. An instruction that the compiler does not look into:
+// it would have every transposing read wait for all loads to LDS. The waits
+// are those of the waves' meetings.
+__device__ __forceinline__ void load_to_lds(i32x4 buffer, uint32_t offset, char* to)
+{
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((ZERO_L char*)to));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(at), "v"(offset), "s"(buffer) : "memory");
+}
 
 // 8 summed elements for this lane's row or column of a piece of 16, from a tile
 // in LDS; `at` is the lane's own place in it, see lane_place.
 template <bool ALONG, int ROW_BYTES>
-__device__ __forceinline__ bf16x8 read_piece(const char* at)
+__device__ __forceinline__ i32x4 read_piece(const char* at)
 {
     if constexpr (ALONG) {
-        return *reinterpret_cast<const bf16x8*>(at);
+        return *reinterpret_cast<const i32x4*>(at);
     } else {
         const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZERO_L i16x4*)at);
         const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZERO_L i16x4*)(at + 4 * ROW_BYTES));
-        return __builtin_bit_cast(bf16x8, (i16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        return __builtin_bit_cast(i32x4, (i16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
+}
+
+// sum += b a for a piece of 16 x 16, in place. The compiler's own form of the
+// instruction may write its sum to other registers than it reads it from, and
+// where its surroundings are held in an order, as below, it then moves and
+// spills sums. As an instruction that it does not look into, this one waits
+// itself for what was written just before; settle() does for what is read of
+// the sums after the last one.
+__device__ __forceinline__ void add_product(f32x4& sum, i32x4 b, i32x4 a)
+{
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(sum) : "v"(b), "v"(a));
+}
+template <int N>
+__device__ __forceinline__ void settle(f32x4 (&sums)[N])
+{
+    asm volatile("s_nop 15\n\ts_nop 15");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+a"(sums[i]));
 }
 
 // Where tile `id` of a grid of tiles lies: it goes down 8 rows of tiles before
@@ -202,8 +235,8 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
     constexpr bool kAlongA = KIND != kFfnWeight, kAlongB = KIND == kFfnForward;
     using A = Factor<kAlongA, T::BM, T::NT>;
     using B = Factor<kAlongB, T::BN, T::NT>;
-    // arrays of their own, so that the compiler sees that a step's reads are not what the next one's loads write
-    __shared__ __align__(16) char sa0[T::BM * BK * 2], sa1[T::BM * BK * 2], sb0[T::BN * BK * 2], sb1[T::BN * BK * 2];
+    constexpr int kDepth = T::DEPTH;
+    __shared__ __align__(16) char tiles[kDepth][(T::BM + T::BN) * BK * 2];
 
     // The first `whole` workgroups take a tile each and all of the summed index;
     // the tiles after these are split over it. Consecutive workgroups go to the
@@ -229,8 +262,9 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
 
     // The units that this thread loads: one place of a row, every kStep-th row.
-    const int row_a = tid / A::kUnits, unit_a = A::place(row_a, tid % A::kUnits);
-    const int row_b = tid / B::kUnits, unit_b = B::place(row_b, tid % B::kUnits);
+    const int row_a = tid / A::kUnits, row_b = tid / B::kUnits;
+    const auto unit_a = [&](int i) { return A::place(row_a + i * A::kStep, tid % A::kUnits); };
+    const auto unit_b = [&](int i) { return B::place(row_b + i * B::kStep, tid % B::kUnits); };
     // forward the second half of B's rows are those of up
     constexpr int kHalfB = KIND == kFfnForward ? B::kVecs / 2 : B::kVecs;
     // Rows beyond the last one are read as the last one, columns as the last
@@ -242,7 +276,7 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
     for (int i = 0; i < A::kVecs; ++i) {
         const int64_t ld = KIND == kFfnForward ? a.ld_h : a.ld_d[which];
         const int64_t row = kAlongA ? min(static_cast<int64_t>(row_a + i * A::kStep), m_end - 1 - m0) : row_a + i * A::kStep;
-        const int64_t col = kAlongA ? unit_a * 8 : min(static_cast<int64_t>(unit_a * 8), m_end - 8 - m0);
+        const int64_t col = kAlongA ? unit_a(i) * 8 : min(static_cast<int64_t>(unit_a(i) * 8), m_end - 8 - m0);
         off_a[i] = static_cast<uint32_t>((row * ld + col + 8) * 2);
     }
 #pragma unroll
@@ -250,12 +284,13 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
         const int64_t ld = KIND == kFfnWeight ? a.ld_h : a.ld_w[KIND == kFfnForward && i >= kHalfB ? 1 : 0];
         const int r = row_b + i % kHalfB * B::kStep;
         const int64_t row = kAlongB ? min(static_cast<int64_t>(r), n_end - 1 - n0) : r;
-        const int64_t col = kAlongB ? unit_b * 8 : min(static_cast<int64_t>(unit_b * 8), n_end - 8 - n0);
+        const int64_t col = kAlongB ? unit_b(i) * 8 : min(static_cast<int64_t>(unit_b(i) * 8), n_end - 8 - n0);
         off_b[i] = static_cast<uint32_t>((row * ld + col + 8) * 2);
     }
-    const int over_a = static_cast<int>(unit_a * 8 - (m_end - 8 - m0)), over_b = static_cast<int>(unit_b * 8 - (n_end - 8 - n0));
-    const int shift_a = !FAST && !kAlongA && over_a > 0 && over_a < 8 ? over_a : 0;
-    const int shift_b = !FAST && !kAlongB && over_b > 0 && over_b < 8 ? over_b : 0;
+    const auto shift_of = [](int64_t over) { return over > 0 && over < 8 ? static_cast<int>(over) : 0; };
+    // (read once: not in every step, whose waits would then wait for them)
+    const uint16_t* const d_which = a.d[which];
+    const int64_t ld_which = a.ld_d[which];
     struct Step {
         const uint16_t *a, *b0, *b1;
         int64_t left;  // summed elements from this step on
@@ -273,60 +308,70 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
             t.a = a.d[seg] + m0 * a.ld_d[seg] + k0;
             t.b0 = t.b1 = a.w[seg] + k0 * a.ld_w[seg] + n0;
         } else {
-            t.a = a.d[which] + k0 * a.ld_d[which] + m0;
+            t.a = d_which + k0 * ld_which + m0;
             t.b0 = t.b1 = a.h + k0 * a.ld_h + n0;
         }
         return t;
     };
     // A step's tiles straight to LDS. (In the last one, elements beyond the sum are read from beyond the buffer: zeros.)
-    const auto send = [&](int64_t s, char* sa, char* sb) {
+    constexpr int kLoads = A::kVecs + B::kVecs;
+    struct Sources {
+        i32x4 a, b0, b1;
+        int left;
+    };
+    const auto sources = [&](int64_t s) {
         const Step t = step_at(s);
-        const __amdgpu_buffer_rsrc_t ra = buffer_at(t.a - 8), rb0 = buffer_at(t.b0 - 8), rb1 = buffer_at(t.b1 - 8);
-        const auto load = [&](int i, bool b, uint32_t off) {
-            char* to = (b ? sb : sa) + (i * T::NT + wave * 64) * 16;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(!b ? ra : i < kHalfB ? rb0 : rb1, (ZERO_L void*)to, 16, off, 0, 0, 0);
-        };
-        if (t.left >= BK) {
-#pragma unroll
-            for (int i = 0; i < A::kVecs; ++i) load(i, false, off_a[i]);
-#pragma unroll
-            for (int i = 0; i < B::kVecs; ++i) load(i, true, off_b[i]);
+        return Sources{buffer_at(t.a - 8), buffer_at(t.b0 - 8), buffer_at(t.b1 - 8), static_cast<int>(min(t.left, int64_t{BK}))};
+    };
+    // load `l` of a step; whole_step: none of it is beyond the sum
+    const auto send_one = [&](const Sources& t, char* to, int l, bool whole_step) {
+        if (l < A::kVecs) {
+            const uint32_t off = whole_step || (kAlongA ? unit_a(l) * 8 : row_a + l * A::kStep) < t.left ? off_a[l] : kBeyond;
+            load_to_lds(t.a, off, to + (l * T::NT + wave * 64) * 16);
         } else {
-#pragma unroll
-            for (int i = 0; i < A::kVecs; ++i) load(i, false, (kAlongA ? unit_a * 8 : row_a + i * A::kStep) >= t.left ? kBeyond : off_a[i]);
-#pragma unroll
-            for (int i = 0; i < B::kVecs; ++i) load(i, true, (kAlongB ? unit_b * 8 : row_b + i * B::kStep) >= t.left ? kBeyond : off_b[i]);
+            const int i = l - A::kVecs;
+            const uint32_t off = whole_step || (kAlongB ? unit_b(i) * 8 : row_b + i * B::kStep) < t.left ? off_b[i] : kBeyond;
+            load_to_lds(i < kHalfB ? t.b0 : t.b1, off, to + T::BM * BK * 2 + (i * T::NT + wave * 64) * 16);
         }
     };
-    // Or through registers, where the rows of an operand do not all lie on 16 bytes.
-    u32x4 va[A::kVecs], vb[B::kVecs];
+    const auto send = [&](int64_t s, char* to) {
+        const Sources t = sources(s);
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) send_one(t, to, l, false);
+    };
+    // Or through registers, where the rows of an operand do not all lie on 16
+    // bytes: two steps' units, so that their loads are in flight as long.
+    struct Units {
+        u32x4 a[A::kVecs], b[B::kVecs];
+    };
     // Steps that are whole go with their loads in flight over a step.
     const auto in_flight = [&](int64_t left) { return a.plain != 0 && left >= BK; };
-    const auto fetch = [&](int64_t s) {
+    const auto fetch = [&](int64_t s, Units& v) {
         const Step t = step_at(s);
         if (!in_flight(t.left)) return;
         const char *pa = reinterpret_cast<const char*>(t.a - 8), *pb0 = reinterpret_cast<const char*>(t.b0 - 8), *pb1 = reinterpret_cast<const char*>(t.b1 - 8);
 #pragma unroll
-        for (int i = 0; i < A::kVecs; ++i) va[i] = ld16_a2(pa + off_a[i]);
+        for (int i = 0; i < A::kVecs; ++i) v.a[i] = ld16_a2(pa + off_a[i]);
 #pragma unroll
-        for (int i = 0; i < B::kVecs; ++i) vb[i] = ld16_a2((i < kHalfB ? pb0 : pb1) + off_b[i]);
+        for (int i = 0; i < B::kVecs; ++i) v.b[i] = ld16_a2((i < kHalfB ? pb0 : pb1) + off_b[i]);
     };
     // What fetch(s) read, to its tiles; or the step's units one after the other, each no further than its row goes.
-    const auto stage = [&](int64_t s, char* sa, char* sb) {
+    const auto stage = [&](int64_t s, Units& v, char* to) {
         const Step t = step_at(s);
+        char* to_b = to + T::BM * BK * 2;
         if (in_flight(t.left)) {
             if (!kAlongA && m0 + T::BM > m_end) {
 #pragma unroll
-                for (int i = 0; i < A::kVecs; ++i) va[i] = shift_unit(va[i], shift_a);
+                for (int i = 0; i < A::kVecs; ++i) v.a[i] = shift_unit(v.a[i], shift_of(unit_a(i) * 8 - (m_end - 8 - m0)));
             }
             if (!kAlongB && n0 + S::kCols > n_end) {
 #pragma unroll
-                for (int i = 0; i < B::kVecs; ++i) vb[i] = shift_unit(vb[i], shift_b);
+                for (int i = 0; i < B::kVecs; ++i) v.b[i] = shift_unit(v.b[i], shift_of(unit_b(i) * 8 - (n_end - 8 - n0)));
             }
 #pragma unroll
-            for (int i = 0; i < A::kVecs; ++i) *reinterpret_cast<u32x4*>(sa + (i * T::NT + tid) * 16) = va[i];
+            for (int i = 0; i < A::kVecs; ++i) *reinterpret_cast<u32x4*>(to + (i * T::NT + tid) * 16) = v.a[i];
 #pragma unroll
-            for (int i = 0; i < B::kVecs; ++i) *reinterpret_cast<u32x4*>(sb + (i * T::NT + tid) * 16) = vb[i];
+            for (int i = 0; i < B::kVecs; ++i) *reinterpret_cast<u32x4*>(to_b + (i * T::NT + tid) * 16) = v.b[i];
             return;
         }
         const int seg = KIND == kFfnInput && s >= seg_steps ? 1 : 0;
@@ -335,120 +380,172 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
             const int row = row_a + i * A::kStep;
             const int64_t ld = KIND == kFfnForward ? a.ld_h : a.ld_d[KIND == kFfnInput ? seg : which];
             u32x4 v{};
-            if (row < (kAlongA ? m_end - m0 : t.left)) v = load_unit(t.a + row * ld, unit_a * 8, kAlongA ? t.left : m_end - m0);
-            *reinterpret_cast<u32x4*>(sa + (i * T::NT + tid) * 16) = v;
+            if (row < (kAlongA ? m_end - m0 : t.left)) v = load_unit(t.a + row * ld, unit_a(i) * 8, kAlongA ? t.left : m_end - m0);
+            *reinterpret_cast<u32x4*>(to + (i * T::NT + tid) * 16) = v;
         }
 #pragma unroll 1
         for (int i = 0; i < B::kVecs; ++i) {
             const int up = i < kHalfB ? 0 : 1, row = row_b + (i - up * kHalfB) * B::kStep;
             const int64_t ld = KIND == kFfnWeight ? a.ld_h : a.ld_w[KIND == kFfnInput ? seg : up];
             u32x4 v{};
-            if (row < (kAlongB ? n_end - n0 : t.left)) v = load_unit((up ? t.b1 : t.b0) + row * ld, unit_b * 8, kAlongB ? t.left : n_end - n0);
-            *reinterpret_cast<u32x4*>(sb + (i * T::NT + tid) * 16) = v;
+            if (row < (kAlongB ? n_end - n0 : t.left)) v = load_unit((up ? t.b1 : t.b0) + row * ld, unit_b(i) * 8, kAlongB ? t.left : n_end - n0);
+            *reinterpret_cast<u32x4*>(to_b + (i * T::NT + tid) * 16) = v;
         }
     };
 
     // Where this lane reads. The four groups of 16 lanes take summed elements 8 g
     // .. 8 g + 7 of 32. ALONG, a lane reads them of row lane % 16 of a piece;
     // across, the 16 lanes of a group read 4 elements' rows, 4 columns a lane, and
-    // get a column of all 4 each.
+    // get a column of all 4 each. There the lane's part of the address and the
+    // piece's meet by exclusive or in the bits that are permuted.
     const int wm = wave / T::WN, wn = wave % T::WN, group = lane / 16, in_group = lane % 16;
-    // In both layouts the lane's part of the address and the piece's meet in
-    // different bits, or by exclusive or in the bits that are permuted.
     const int across_row = 8 * group + in_group / 4;
-    uint32_t at_a, at_b;  // of piece 0, summed element 0
+    constexpr int kColsB = S::kCols / T::WN;  // forward a wave's first pieces are of gate, the others of as many columns of up
+    uint32_t at_a, at_b;  // of piece 0
     if constexpr (kAlongA) at_a = (wm * (T::BM / T::WM) + in_group) * A::kRowBytes + A::place(in_group, group) * 16;
     else at_a = across_row * A::kRowBytes + A::place(across_row, wm * (T::BM / T::WM) / 8) * 16 + in_group % 4 * 8;
-    constexpr int kColsB = S::kCols / T::WN;  // forward a wave's first pieces are of gate, the others of as many columns of up
     if constexpr (kAlongB) at_b = (wn * kColsB + in_group) * B::kRowBytes + B::place(in_group, group) * 16;
     else at_b = across_row * B::kRowBytes + B::place(across_row, wn * kColsB / 8) * 16 + in_group % 4 * 8;
-    const auto piece_a = [&](const char* sa, int i, int k) {
-        if constexpr (kAlongA) return sa + ((at_a ^ k * 2) + 16 * i * A::kRowBytes);
-        else return sa + ((at_a ^ i * 32) + k * A::kRowBytes);
-    };
-    const auto piece_b = [&](const char* sb, int j, int k) {
-        if constexpr (kAlongB) {
-            const int row = 16 * j + (KIND == kFfnForward && j >= T::TN / 2 ? T::BN / 2 - T::TN * 8 : 0);
-            return sb + ((at_b ^ k * 2) + row * B::kRowBytes);
-        } else return sb + ((at_b ^ j * 32) + k * B::kRowBytes);
-    };
     f32x4 acc[T::TN][T::TM];
 #pragma unroll
     for (int j = 0; j < T::TN; ++j)
 #pragma unroll
-        for (int i = 0; i < T::TM; ++i) acc[j][i] = f32x4{};
-    struct Half {  // of a step: the pieces of 32 summed elements
-        bf16x8 a[T::TM], b[T::TN];
+        for (int i = 0; i < T::TM; ++i) {
+            acc[j][i] = f32x4{};
+            asm volatile("" : "+a"(acc[j][i]));
+        }
+    // The pieces of the factor of which a wave has few are read first; those of
+    // the other are multiplied with them one after the other, in the order in
+    // which the next step's are read.
+    constexpr bool kManyB = T::TN > T::TM;
+    constexpr int kMany = kManyB ? T::TN : T::TM, kFew = kManyB ? T::TM : T::TN, kProducts = kMany * kFew;
+    struct Pieces {
+        i32x4 few[kFew], many[kMany];
     };
-    const auto read = [&](Half& h, const char* sa, const char* sb, int k) {
+    const auto read_a = [&](const char* from, int i) {
+        if constexpr (kAlongA) return read_piece<true, A::kRowBytes>(from + at_a + 16 * i * A::kRowBytes);
+        else return read_piece<false, A::kRowBytes>(from + (at_a ^ i * 32));
+    };
+    const auto read_b = [&](const char* from, int j) {
+        from += T::BM * BK * 2;
+        if constexpr (kAlongB) {
+            const int row = 16 * j + (KIND == kFfnForward && j >= T::TN / 2 ? T::BN / 2 - T::TN * 8 : 0);
+            return read_piece<true, B::kRowBytes>(from + at_b + row * B::kRowBytes);
+        } else return read_piece<false, B::kRowBytes>(from + (at_b ^ j * 32));
+    };
+    const auto read_one = [&](Pieces& h, const char* from, int q) {
         // (kept from the compiler, which would hold the address of every piece in a register)
         asm volatile("" : "+v"(at_a), "+v"(at_b));
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) h.b[j] = read_piece<kAlongB, B::kRowBytes>(piece_b(sb, j, k));
-#pragma unroll
-        for (int i = 0; i < T::TM; ++i) h.a[i] = read_piece<kAlongA, A::kRowBytes>(piece_a(sa, i, k));
+        if (q < kFew) h.few[q] = kManyB ? read_a(from, q) : read_b(from, q);
+        else h.many[q - kFew] = kManyB ? read_b(from, q - kFew) : read_a(from, q - kFew);
     };
-    const auto multiply = [&](const Half& h) {
+    const auto read = [&](Pieces& h, const char* from) {
 #pragma unroll
-        for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-            for (int j = 0; j < T::TN; ++j) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h.b[j], h.a[i], acc[j][i], 0, 0, 0);
+        for (int q = 0; q < kFew + kMany; ++q) read_one(h, from, q);
     };
-    // This wave's loads to LDS have arrived and its reads and writes of it are done, and so are all waves'.
-    const auto meet = [&] {
+    const auto multiply_one = [&](const Pieces& h, int t) {
+        const int x = t / kFew, y = t % kFew;
+        if (kManyB) add_product(acc[x][y], h.many[x], h.few[y]);
+        else add_product(acc[y][x], h.few[y], h.many[x]);
+    };
+    const auto multiply = [&](const Pieces& h) {
+#pragma unroll
+        for (int t = 0; t < kProducts; ++t) multiply_one(h, t);
+    };
+    // The waves meet: all reads of LDS are done, and writes, and all loads to LDS
+    // but those of the last LATER steps that were sent.
+    const auto meet = [&](auto later) {
+        constexpr int kPending = FAST ? decltype(later)::value * kLoads : 63;
+        static_assert(kPending < 64, "the counter has six bits");
         __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kPending) : "memory");
+        __builtin_amdgcn_s_waitcnt(15 | 7 << 4 | 3 << 14);  // lgkmcnt(0) alone
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    // A step, of which the first half is in registers already. Its second half
-    // is read while the first is multiplied. With that the step's tiles are free
-    // for the step after the next, whose loads are then in flight for a step, and
-    // the next one's have arrived: its first half is read while the second half is
-    // multiplied. So the waves meet once a step, with products on both sides.
-    Half h0, h1;
-    const auto step = [&](int64_t s, char* sa, char* sb, char* next_a, char* next_b) {
-        read(h1, sa, sb, 32);
-        multiply(h0);
+    // A step, whose pieces are in registers or on their way there. Once they have
+    // come, in every wave, the step's tiles are free for the step kDepth later,
+    // and the next step's tiles have arrived: its pieces are read while this
+    // step's are multiplied. A load to LDS is in flight for kDepth - 1 steps.
+    // u: the step's number modulo kDepth and 2.
+    Pieces p[2];
+    Units v[2];
+    constexpr int kUnroll = kDepth % 2 ? 2 * kDepth : kDepth;
+    const auto step = [&](int64_t s, int u) {
+        if (s + kDepth <= end) meet(std::integral_constant<int, kDepth - 2>{});
+        else meet(std::integral_constant<int, 0>{});
         if constexpr (FAST) {
-            meet();
-            if (s + 2 < end) send(s + 2, sa, sb);
+            if (s + kDepth < end) send(s + kDepth, tiles[u % kDepth]);
         } else {
-            // (only the reads and writes of LDS: the loads to registers go on)
-            __builtin_amdgcn_sched_barrier(0);
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
-            if (s + 2 < end) stage(s + 2, sa, sb);
-            if (s + 3 < end) fetch(s + 3);
+            if (s + 2 < end) stage(s + 2, v[u % 2], tiles[u % 2]);
+            if (s + 4 < end) fetch(s + 4, v[u % 2]);
         }
-        if (s + 1 < end) read(h0, next_a, next_b, 0);
-        multiply(h1);
-        __builtin_amdgcn_sched_barrier(0);
+        if (s + 1 < end) read(p[(u + 1) % 2], tiles[(u + 1) % kDepth]);
+        multiply(p[u % 2]);
     };
+    static_assert(FAST || kDepth == 2, "through registers two steps lie in LDS");
     if (begin < end) {
         if constexpr (FAST) {
-            send(begin, sa0, sb0);
-            if (begin + 1 < end) send(begin + 1, sa1, sb1);
+#pragma unroll
+            for (int u = 0; u < kDepth; ++u)
+                if (begin + u < end) send(begin + u, tiles[u]);
+            if (begin + kDepth <= end) meet(std::integral_constant<int, kDepth - 1>{});
+            else meet(std::integral_constant<int, 0>{});
         } else {
-            fetch(begin);
-            stage(begin, sa0, sb0);
+            fetch(begin, v[0]);
+            stage(begin, v[0], tiles[0]);
             if (begin + 1 < end) {
-                fetch(begin + 1);
-                stage(begin + 1, sa1, sb1);
+                fetch(begin + 1, v[1]);
+                stage(begin + 1, v[1], tiles[1]);
             }
-            if (begin + 2 < end) fetch(begin + 2);
+            if (begin + 2 < end) fetch(begin + 2, v[0]);
+            if (begin + 3 < end) fetch(begin + 3, v[1]);
+            meet(std::integral_constant<int, 0>{});
         }
-        meet();
-        read(h0, sa0, sb0, 0);
+        read(p[0], tiles[0]);
     }
-    for (int64_t s = begin; s < end; s += 2) {
-        step(s, sa0, sb0, sa1, sb1);
-        if (s + 1 < end) step(s + 1, sa1, sb1, sa0, sb0);
+    // Before which product a piece of the next step is read: the few and the first
+    // two of the many at once, each other one when an earlier one's products have
+    // freed as many registers; and the loads are sent behind these. (Products are
+    // in the order that they are written in, and reads and loads stay between
+    // them. Left to itself the compiler reads as late as it can, to save
+    // registers, and the waves then meet waiting.)
+    constexpr int kFirst = kFew + 2, kRead = 2 * kFew + (kMany - 2) * (kFew > 1 ? kFew - 1 : 1);
+    const auto read_at = [](int q) { return q < kFirst ? q * 2 * kFew / kFirst : 2 * kFew + (q - kFirst) * (kFew > 1 ? kFew - 1 : 1); };
+    const auto send_at = [](int l) { return kRead + l * (kProducts - kRead) / kLoads; };
+    int64_t s = begin;
+    if constexpr (FAST) {
+        // Steps in which nothing is asked, up to one that sends one that is not whole.
+        const int64_t asked = k_end % BK == 0 ? end : KIND == kFfnInput ? min(end, seg_steps - 1) : min(end, all_steps - 1);
+        for (; s + kUnroll + kDepth <= asked; s += kUnroll) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                meet(std::integral_constant<int, kDepth - 2>{});
+                const Sources next = sources(s + u + kDepth);
+#pragma unroll
+                for (int t = 0; t < kProducts; ++t) {
+#pragma unroll
+                    for (int q = 0; q < kFew + kMany; ++q)
+                        if (read_at(q) == t) read_one(p[(u + 1) % 2], tiles[(u + 1) % kDepth], q);
+#pragma unroll
+                    for (int l = 0; l < kLoads; ++l)
+                        if (send_at(l) == t) send_one(next, tiles[u % kDepth], l, true);
+                    multiply_one(p[u % 2], t);
+                }
+            }
+        }
+    }
+    for (; s < end; s += kUnroll) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (s + u >= end) break;
+            step(s + u, u);
+        }
     }
     // the last step's tiles are read, in every wave, since its meeting
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) settle(acc[j]);
 
     // B is the first operand, so a lane holds four neighbouring columns of one
     // row of the output. Sixteen rows at a time go through LDS (each wave its own
@@ -459,10 +556,8 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
     // accesses are in order.
     constexpr int kWide = T::TN * 16, kOut = KIND == kFfnForward ? kWide / 2 : kWide, kLanes = kOut / 8, kPad = kWide + 4;
     static_assert(KIND != kFfnForward || kOut % kActBlock == 0, "a block of 32 columns lies in one wave");
-    constexpr int kRoom = (T::NT / 64 + 3) / 4 * 16 * kPad * 4;  // of a fourth of the waves
-    static_assert(kRoom <= sizeof(sb0) && (T::NT <= 128 || kRoom <= sizeof(sa0)), "each array holds 16 rows of a fourth of the waves");
-    const int quarter = wave % 4;
-    float* out = reinterpret_cast<float*>(quarter == 0 ? sb0 : quarter == 1 ? sb1 : quarter == 2 ? sa0 : sa1) + wave / 4 * 16 * kPad;
+    static_assert(T::NT / 64 * 16 * kPad * 4 <= sizeof(tiles), "LDS holds 16 rows of every wave");
+    float* out = reinterpret_cast<float*>(&tiles[0][0]) + wave * 16 * kPad;
     const int64_t n = n0 + wn * kOut + lane % kLanes * 8;
     const int left = static_cast<int>(min(n_end - n, int64_t{8}));
 #pragma unroll
@@ -545,12 +640,11 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(FfnArgs a, int tiles_m, i
 // Forward a wave's columns of gate, and as many of up, are 64 or 32, a line of
 // each; otherwise its 128 x 64 sums read the fewest pieces.
 template <FfnKind KIND>
-using Big = Tile<256, 256, KIND == kFfnForward ? 4 : 2, KIND == kFfnForward ? 2 : 4, 1>;
-using Mid = Tile<128, 128, 2, 2, 2>;
-using Small = Tile<64, 128, 2, 2, 3>;
-template <FfnKind KIND>
-using Flat = Tile<32, 128, 1, KIND == kFfnForward ? 2 : 4, 4>;
-using Slow = Tile<128, 128, 2, 2, 2>;  // through registers
+using Big = Tile<256, 256, KIND == kFfnForward ? 4 : 2, KIND == kFfnForward ? 2 : 4, 4, 1>;
+using Mid = Tile<128, 128, 2, 2, 4, 2>;
+using Small = Tile<64, 128, 2, 2, 4, 3>;
+using Flat = Tile<32, 128, 1, 2, 4, 4>;
+using Slow = Tile<128, 128, 2, 2, 2, 2>;  // through registers
 
 // Whether 32-bit offsets reach over the 256 rows of a tile, the same ones in
 // both segments, and what runs across the summed index has a whole unit.
@@ -617,7 +711,7 @@ enum TileId { kBig, kMid, kSmall, kFlat, kSlow };
 
 FfnPlan plan_for(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t hidden)
 {
-    static const Candidate kTiles[] = {candidate<Flat<kFfnForward>>(kFlat, 0.60, 3.3), candidate<Small>(kSmall, 0.70, 1.3),
+    static const Candidate kTiles[] = {candidate<Flat>(kFlat, 0.60, 3.3), candidate<Small>(kSmall, 0.70, 1.3),
                                        candidate<Mid>(kMid, 0.85, 1.2), candidate<Big<kFfnForward>>(kBig, 1.6, 1.7)};
     static const Candidate kSlowTile = candidate<Slow>(kSlow, 1.5, 2.0);
     constexpr double kStart = 4.0, kJoin = 5.0, kBytes = 2e6;  // us a round, us a join, bytes of parts written and read a us
@@ -682,7 +776,7 @@ hipError_t launch_kind(FfnArgs a, hipStream_t s)
     }
     if constexpr (KIND != kFfnWeight) {  // its columns' tiles are 128 or more: their units are permuted by pairs of eight
         if (plan.tile == kSmall) return launch_tile<Small, KIND, true>(a, plan, s);
-        return launch_tile<Flat<KIND>, KIND, true>(a, plan, s);
+        return launch_tile<Flat, KIND, true>(a, plan, s);
     }
     return hipErrorInvalidValue;
 }
