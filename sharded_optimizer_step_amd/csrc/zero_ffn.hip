@@ -9,6 +9,7 @@
 // factors of the weight gradients) the tile lies as in memory and the
 // transposing LDS reads turn it.
 #include <type_traits>
+#include <utility>
 
 #include "zero_act8_device.h"
 
@@ -24,7 +25,8 @@ constexpr int BK = 32;  // summed elements of a step
 
 // ------------------------------------------------------------------ activations
 
-// 1 / (1 + exp(-x)), within 3 units of its last place and |x| 2^-24 of itself
+// The forms of a kernel whose instructions all waves fetch: short, without
+// branches. 1 / (1 + exp(-x)), within 3 units of its last place and |x| 2^-24 of itself
 // (what is made of it is rounded to bf16 or 8 bits). For large |x| the
 // exponential is infinite or 0, and the result the limit.
 __device__ __forceinline__ float logistic(float x)
@@ -32,11 +34,29 @@ __device__ __forceinline__ float logistic(float x)
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }
 
-__device__ __forceinline__ float activation(int act, float g)
+// f = act(f) u for 8 values, all of them at once: their exponentials and
+// reciprocals do not wait for each other.
+__device__ __forceinline__ void gated(int act, float (&f)[8], const float (&u)[8])
 {
-    if (act == ZERO_FFN_SILU) return g * logistic(g);
-    if (act == ZERO_FFN_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678f));
-    return g * logistic(1.59576912f * fmaf(0.044715f * g * g, g, g));  // (1 + tanh(z)) / 2 is the logistic function of 2 z
+    float p[8];
+    if (act == ZERO_FFN_SILU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = logistic(f[i]);
+    } else if (act == ZERO_FFN_GELU) {
+        // erfc(x) for x >= 0 as exp(-x^2) times a polynomial of 1 / (1 + p x), within 1.5e-7 (Abramowitz and Stegun, 7.1.26)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = fabsf(f[i]) * 0.70710678f, t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+            const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+            const float half = 0.5f * poly * __builtin_amdgcn_exp2f(x * x * -1.44269504f);
+            p[i] = f[i] > 0.0f ? 1.0f - half : half;
+        }
+    } else {  // (1 + tanh(z)) / 2 is the logistic function of 2 z
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = logistic(1.59576912f * fmaf(0.044715f * f[i] * f[i], f[i], f[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] * p[i] * u[i];
 }
 
 // ------------------------------------------------------------------ tiles in LDS
@@ -115,13 +135,14 @@ __device__ __forceinline__ i32x4 buffer_at(const uint16_t* p)
 constexpr uint32_t kBeyond = 0xFFFFFF00u;
 
 // 16 bytes a lane from `offset` of a buffer to LDS, a wave's 64 units one after
-// the other from `to` on. An instruction that the compiler does not look into:
+// the other from base + TO on. An instruction that the compiler does not look into:
 // it would have every transposing read wait for all loads to LDS. The waits
 // are those of the waves' meetings.
-__device__ __forceinline__ void load_to_lds(i32x4 buffer, uint32_t offset, char* to)
+template <int TO>
+__device__ __forceinline__ void load_to_lds(i32x4 buffer, uint32_t offset, uint32_t base)
 {
-    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((ZERO_L char*)to));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(at), "v"(offset), "s"(buffer) : "memory");
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 : : "s"(base), "v"(offset), "s"(buffer), "n"(TO) : "memory", "scc");
 }
 
 // 8 summed elements for this lane's row or column of a piece of 16, from a tile
@@ -141,12 +162,13 @@ __device__ __forceinline__ i32x4 read_piece(const char* at)
 // sum += b a for a piece of 16 x 16, in place. The compiler's own form of the
 // instruction may write its sum to other registers than it reads it from, and
 // where its surroundings are held in an order, as below, it then moves and
-// spills sums. As an instruction that it does not look into, this one waits
-// itself for what was written just before; settle() does for what is read of
-// the sums after the last one.
+// spills sums. It does not look into this one and so waits for nothing on its
+// behalf: not for a vector instruction that wrote an operand within the two
+// instructions before (there are none: operands come from LDS, a test of the
+// assembly says so), nor for what reads the sums after the last one: settle().
 __device__ __forceinline__ void add_product(f32x4& sum, i32x4 b, i32x4 a)
 {
-    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(sum) : "v"(b), "v"(a));
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(sum) : "v"(b), "v"(a));
 }
 template <int N>
 __device__ __forceinline__ void settle(f32x4 (&sums)[N])
@@ -154,6 +176,18 @@ __device__ __forceinline__ void settle(f32x4 (&sums)[N])
     asm volatile("s_nop 15\n\ts_nop 15");
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+a"(sums[i]));
+}
+
+// f(0), f(1), .. f(N - 1) with numbers that are constants.
+template <class F, int... I>
+__device__ __forceinline__ void unrolled_of(F&& f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F&& f)
+{
+    unrolled_of(f, std::make_integer_sequence<int, N>{});
 }
 
 // Where tile `id` of a grid of tiles lies: it goes down 8 rows of tiles before
@@ -196,8 +230,7 @@ __device__ __forceinline__ void finish(const FfnArgs& a, int which, int64_t m, i
         if (left <= 0) return;
         if (a.out[0].p != nullptr) store8<false, true>(a.out[0], m, n, left, f);
         if (a.out[1].p != nullptr) store8<false, true>(a.out[1], m, n, left, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = activation(a.act, f[i]) * u[i];
+        gated(a.act, f, u);
         store8<false, true>(a.a, m, n, left, f);
     } else {
         if (left <= 0) return;
@@ -313,31 +346,46 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
         }
         return t;
     };
-    // A step's tiles straight to LDS. (In the last one, elements beyond the sum are read from beyond the buffer: zeros.)
+    // The step whose tiles are sent next, straight to LDS. (In the last one of a
+    // sum, elements beyond it are read from beyond the buffer: zeros.)
     constexpr int kLoads = A::kVecs + B::kVecs;
-    struct Sources {
-        i32x4 a, b0, b1;
-        int left;
-    };
-    const auto sources = [&](int64_t s) {
+    struct Cursor {
+        const uint16_t *a, *b0, *b1;
+        int64_t left, to_switch;  // summed elements left in this sum; steps to the second sum
+    } cursor;
+    const int64_t step_a = kAlongA ? BK : BK * (KIND == kFfnWeight ? ld_which : a.ld_d[0]);
+    const int64_t step_b = kAlongB ? BK : BK * (KIND == kFfnWeight ? a.ld_h : a.ld_w[0]);
+    const auto point_at = [&](int64_t s) {
         const Step t = step_at(s);
-        return Sources{buffer_at(t.a - 8), buffer_at(t.b0 - 8), buffer_at(t.b1 - 8), static_cast<int>(min(t.left, int64_t{BK}))};
+        cursor = Cursor{t.a - 8, t.b0 - 8, t.b1 - 8, t.left, seg_steps - s};
     };
-    // load `l` of a step; whole_step: none of it is beyond the sum
-    const auto send_one = [&](const Sources& t, char* to, int l, bool whole_step) {
-        if (l < A::kVecs) {
-            const uint32_t off = whole_step || (kAlongA ? unit_a(l) * 8 : row_a + l * A::kStep) < t.left ? off_a[l] : kBeyond;
-            load_to_lds(t.a, off, to + (l * T::NT + wave * 64) * 16);
-        } else {
-            const int i = l - A::kVecs;
-            const uint32_t off = whole_step || (kAlongB ? unit_b(i) * 8 : row_b + i * B::kStep) < t.left ? off_b[i] : kBeyond;
-            load_to_lds(i < kHalfB ? t.b0 : t.b1, off, to + T::BM * BK * 2 + (i * T::NT + wave * 64) * 16);
+    const auto advance = [&] {
+        cursor.a += step_a;
+        cursor.b0 += step_b;
+        cursor.b1 += step_b;
+        cursor.left -= BK;
+        if constexpr (KIND == kFfnInput) {
+            if (--cursor.to_switch == 0) point_at(seg_steps);
         }
     };
-    const auto send = [&](int64_t s, char* to) {
-        const Sources t = sources(s);
-#pragma unroll
-        for (int l = 0; l < kLoads; ++l) send_one(t, to, l, false);
+    const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((ZERO_L char*)&tiles[0][0])) + wave * 1024;
+    // load L of a step to slot U of the ring; WHOLE: none of it is beyond the sum
+    const auto send_one = [&](auto slot, auto number, auto whole_step) {
+        constexpr int U = decltype(slot)::value, L = decltype(number)::value;
+        constexpr bool WHOLE = decltype(whole_step)::value;
+        constexpr int kSlot = U * (T::BM + T::BN) * BK * 2;
+        if constexpr (L < A::kVecs) {
+            const uint32_t off = WHOLE || (kAlongA ? unit_a(L) * 8 : row_a + L * A::kStep) < cursor.left ? off_a[L] : kBeyond;
+            load_to_lds<kSlot + L * T::NT * 16>(buffer_at(cursor.a), off, lds_base);
+        } else {
+            constexpr int I = L - A::kVecs;
+            const uint32_t off = WHOLE || (kAlongB ? unit_b(I) * 8 : row_b + I * B::kStep) < cursor.left ? off_b[I] : kBeyond;
+            load_to_lds<kSlot + T::BM * BK * 2 + I * T::NT * 16>(buffer_at(I < kHalfB ? cursor.b0 : cursor.b1), off, lds_base);
+        }
+    };
+    const auto send = [&](auto slot) {
+        unrolled<kLoads>([&](auto l) { send_one(slot, l, std::false_type{}); });
+        advance();
     };
     // Or through registers, where the rows of an operand do not all lie on 16
     // bytes: two steps' units, so that their loads are in flight as long.
@@ -434,8 +482,8 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
         } else return read_piece<false, B::kRowBytes>(from + (at_b ^ j * 32));
     };
     const auto read_one = [&](Pieces& h, const char* from, int q) {
-        // (kept from the compiler, which would hold the address of every piece in a register)
-        asm volatile("" : "+v"(at_a), "+v"(at_b));
+        // (kept from the compiler where it would hold the address of every piece in a register that it lacks)
+        if constexpr (T::kWavesASimd > 1) asm volatile("" : "+v"(at_a), "+v"(at_b));
         if (q < kFew) h.few[q] = kManyB ? read_a(from, q) : read_b(from, q);
         else h.many[q - kFew] = kManyB ? read_b(from, q - kFew) : read_a(from, q - kFew);
     };
@@ -448,10 +496,7 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
         if (kManyB) add_product(acc[x][y], h.many[x], h.few[y]);
         else add_product(acc[y][x], h.few[y], h.many[x]);
     };
-    const auto multiply = [&](const Pieces& h) {
-#pragma unroll
-        for (int t = 0; t < kProducts; ++t) multiply_one(h, t);
-    };
+    const auto multiply = [&](const Pieces& h) { unrolled<kProducts>([&](auto t) { multiply_one(h, t); }); };
     // The waves meet: all reads of LDS are done, and writes, and all loads to LDS
     // but those of the last LATER steps that were sent.
     const auto meet = [&](auto later) {
@@ -472,11 +517,11 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
     Pieces p[2];
     Units v[2];
     constexpr int kUnroll = kDepth % 2 ? 2 * kDepth : kDepth;
-    const auto step = [&](int64_t s, int u) {
+    const auto step = [&](int64_t s, auto u) {
         if (s + kDepth <= end) meet(std::integral_constant<int, kDepth - 2>{});
         else meet(std::integral_constant<int, 0>{});
         if constexpr (FAST) {
-            if (s + kDepth < end) send(s + kDepth, tiles[u % kDepth]);
+            if (s + kDepth < end) send(std::integral_constant<int, u % kDepth>{});
         } else {
             if (s + 2 < end) stage(s + 2, v[u % 2], tiles[u % 2]);
             if (s + 4 < end) fetch(s + 4, v[u % 2]);
@@ -487,9 +532,10 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
     static_assert(FAST || kDepth == 2, "through registers two steps lie in LDS");
     if (begin < end) {
         if constexpr (FAST) {
-#pragma unroll
-            for (int u = 0; u < kDepth; ++u)
-                if (begin + u < end) send(begin + u, tiles[u]);
+            point_at(begin);
+            unrolled<kDepth>([&](auto u) {
+                if (begin + u < end) send(u);
+            });
             if (begin + kDepth <= end) meet(std::integral_constant<int, kDepth - 1>{});
             else meet(std::integral_constant<int, 0>{});
         } else {
@@ -507,68 +553,76 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
     }
     // Before which product a piece of the next step is read: the few and the first
     // two of the many at once, each other one when an earlier one's products have
-    // freed as many registers; and the loads are sent behind these. (Products are
+    // freed as many registers; and the loads are sent evenly among them. (Products are
     // in the order that they are written in, and reads and loads stay between
     // them. Left to itself the compiler reads as late as it can, to save
     // registers, and the waves then meet waiting.)
-    constexpr int kFirst = kFew + 2, kRead = 2 * kFew + (kMany - 2) * (kFew > 1 ? kFew - 1 : 1);
-    const auto read_at = [](int q) { return q < kFirst ? q * 2 * kFew / kFirst : 2 * kFew + (q - kFirst) * (kFew > 1 ? kFew - 1 : 1); };
-    const auto send_at = [](int l) { return kRead + l * (kProducts - kRead) / kLoads; };
+    constexpr int kFirst = kFew + 2;
+    constexpr auto read_at = [](int q) { return q < kFirst ? q * 2 * kFew / kFirst : 2 * kFew + (q - kFirst) * (kFew > 1 ? kFew - 1 : 1); };
+    constexpr auto send_at = [](int l) { return (2 * l + 1) * kProducts / (2 * kLoads); };
     int64_t s = begin;
     if constexpr (FAST) {
         // Steps in which nothing is asked, up to one that sends one that is not whole.
         const int64_t asked = k_end % BK == 0 ? end : KIND == kFfnInput ? min(end, seg_steps - 1) : min(end, all_steps - 1);
         for (; s + kUnroll + kDepth <= asked; s += kUnroll) {
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+            unrolled<kUnroll>([&](auto u) {
                 meet(std::integral_constant<int, kDepth - 2>{});
-                const Sources next = sources(s + u + kDepth);
-#pragma unroll
-                for (int t = 0; t < kProducts; ++t) {
-#pragma unroll
-                    for (int q = 0; q < kFew + kMany; ++q)
-                        if (read_at(q) == t) read_one(p[(u + 1) % 2], tiles[(u + 1) % kDepth], q);
-#pragma unroll
-                    for (int l = 0; l < kLoads; ++l)
-                        if (send_at(l) == t) send_one(next, tiles[u % kDepth], l, true);
+                unrolled<kProducts>([&](auto t) {
+                    unrolled<kFew + kMany>([&](auto q) {
+                        if constexpr (read_at(q) == t) read_one(p[(u + 1) % 2], tiles[(u + 1) % kDepth], q);
+                    });
+                    unrolled<kLoads>([&](auto l) {
+                        if constexpr (send_at(l) == t) send_one(std::integral_constant<int, u % kDepth>{}, l, std::true_type{});
+                    });
                     multiply_one(p[u % 2], t);
-                }
-            }
+                });
+                advance();
+            });
         }
     }
     for (; s < end; s += kUnroll) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (s + u >= end) break;
-            step(s + u, u);
-        }
+        unrolled<kUnroll>([&](auto u) {
+            if (s + u < end) step(s + u, u);
+        });
     }
     // the last step's tiles are read, in every wave, since its meeting
 #pragma unroll
     for (int j = 0; j < T::TN; ++j) settle(acc[j]);
 
     // B is the first operand, so a lane holds four neighbouring columns of one
-    // row of the output. Sixteen rows at a time go through LDS (each wave its own
-    // part of what the tiles lay in; the last barrier is behind every read of
-    // them), after which a lane has eight neighbouring columns, forward of gate
+    // row of the output. Sixteen rows and more at a time go through LDS (each wave
+    // its own part of what the tiles lay in; the last barrier is behind every read
+    // of them), after which a lane has eight neighbouring columns, forward of gate
     // and of up, and eight lanes whole lines. The fences keep the compiler from
     // moving a lane's reads over its writes, which other lanes read; a wave's LDS
     // accesses are in order.
+    //
+    // The code of the results stands here once, in a loop, and the sums move up to
+    // the pieces that it takes: written out for every piece it is run once a tile
+    // and its instructions come from memory each time (25 us a tile instead of 7).
     constexpr int kWide = T::TN * 16, kOut = KIND == kFfnForward ? kWide / 2 : kWide, kLanes = kOut / 8, kPad = kWide + 4;
+    constexpr int kRoom = sizeof(tiles) / (T::NT / 64) / (16 * kPad * 4);  // pieces of 16 rows
+    constexpr int kAtOnce = kRoom >= T::TM ? T::TM : kRoom >= 2 && T::TM % 2 == 0 ? 2 : 1;
     static_assert(KIND != kFfnForward || kOut % kActBlock == 0, "a block of 32 columns lies in one wave");
-    static_assert(T::NT / 64 * 16 * kPad * 4 <= sizeof(tiles), "LDS holds 16 rows of every wave");
-    float* out = reinterpret_cast<float*>(&tiles[0][0]) + wave * 16 * kPad;
+    static_assert(kRoom >= 1, "LDS holds 16 rows of every wave");
+    float* out = reinterpret_cast<float*>(&tiles[0][0]) + wave * kAtOnce * 16 * kPad;
     const int64_t n = n0 + wn * kOut + lane % kLanes * 8;
     const int left = static_cast<int>(min(n_end - n, int64_t{8}));
-#pragma unroll
-    for (int i = 0; i < T::TM; ++i) {
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) *reinterpret_cast<f32x4*>(out + in_group * kPad + 16 * j + group * 4) = acc[j][i];
+    const int part_col = wn * kOut + lane % kLanes * 8;
+    float* const part_tile = a.part + (static_cast<int64_t>(split_tile) * a.split + part) * (T::BM * T::BN) + part_col;
+#pragma unroll 1
+    for (int first = wm * (T::BM / T::WM); first < (wm + 1) * (T::BM / T::WM); first += 16 * kAtOnce) {
+        unrolled<kAtOnce>([&](auto i) {
+            unrolled<T::TN>([&](auto j) {
+                *reinterpret_cast<f32x4*>(out + (16 * i + in_group) * kPad + 16 * j + group * 4) = acc[j][i];
+            });
+        });
+        unrolled<T::TM - kAtOnce>([&](auto i) { unrolled<T::TN>([&](auto j) { acc[j][i] = acc[j][i + kAtOnce]; }); });
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-        for (int r = 0; r < 16; r += 64 / kLanes) {
-            const int row = r + lane / kLanes, tile_row = wm * (T::BM / T::WM) + 16 * i + row;
-            const int64_t m = m0 + tile_row;
+#pragma unroll 1
+        for (int row = lane / kLanes; row < 16 * kAtOnce; row += 64 / kLanes) {
+            const int64_t m = m0 + first + row;
+            if (m >= m_end) break;  // whole rows
             float f[8], u[8] = {};
             const float* from = out + row * kPad + lane % kLanes * 8;
 #pragma unroll
@@ -576,9 +630,8 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
                 *reinterpret_cast<f32x4*>(f + c) = *reinterpret_cast<const f32x4*>(from + c);
                 if constexpr (KIND == kFfnForward) *reinterpret_cast<f32x4*>(u + c) = *reinterpret_cast<const f32x4*>(from + kOut + c);
             }
-            if (m >= m_end) continue;
             if (parted) {
-                float* to = a.part + (static_cast<int64_t>(split_tile) * a.split + part) * (T::BM * T::BN) + tile_row * T::BN + wn * kOut + lane % kLanes * 8;
+                float* to = part_tile + (first + row) * T::BN;
 #pragma unroll
                 for (int c = 0; c < 8; c += 4) {
                     *(ZERO_G f32x4*)(to + c) = *reinterpret_cast<f32x4*>(f + c);
@@ -640,7 +693,7 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(FfnArgs a, int tiles_m, i
 // Forward a wave's columns of gate, and as many of up, are 64 or 32, a line of
 // each; otherwise its 128 x 64 sums read the fewest pieces.
 template <FfnKind KIND>
-using Big = Tile<256, 256, KIND == kFfnForward ? 4 : 2, KIND == kFfnForward ? 2 : 4, 4, 1>;
+using Big = Tile<256, 256, KIND == kFfnForward ? 4 : 2, 2, 4, 1>;
 using Mid = Tile<128, 128, 2, 2, 4, 2>;
 using Small = Tile<64, 128, 2, 2, 4, 3>;
 using Flat = Tile<32, 128, 1, 2, 4, 4>;
