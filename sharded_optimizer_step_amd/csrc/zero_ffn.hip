@@ -693,7 +693,7 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(FfnArgs a, int tiles_m, i
 // Forward a wave's columns of gate, and as many of up, are 64 or 32, a line of
 // each; otherwise its 128 x 64 sums read the fewest pieces.
 template <FfnKind KIND>
-using Big = Tile<256, 256, KIND == kFfnForward ? 4 : 2, 2, 4, 1>;
+using Big = Tile<256, 256, KIND == kFfnForward ? 4 : 2, 2, KIND == kFfnForward ? 3 : 4, 1>;
 using Mid = Tile<128, 128, 2, 2, 4, 2>;
 using Small = Tile<64, 128, 2, 2, 4, 3>;
 using Flat = Tile<32, 128, 1, 2, 4, 4>;

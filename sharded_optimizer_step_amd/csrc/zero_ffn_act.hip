@@ -16,7 +16,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kUnit = 0x1p-24f;  // half a step of fp32, relative
 
-// act(g) = g p and act'(g) in fp32, within slack_f * |act(g)| and slack_d.
+// act(g) = g p and act'(g) in fp32, within slack_f of itself and slack_d.
 struct Terms {
     float f, d, slack_f, slack_d;
     bool sure;  // the bounds hold
@@ -25,54 +25,58 @@ struct Terms {
 // The bounds count units of 2^-24: one for an operation, two for the
 // instructions of the exponential and the reciprocal, and what the rounding of
 // the exponent's argument adds, its size.
-__device__ __forceinline__ Terms terms(int act, float g)
+template <int ACT>
+__device__ __forceinline__ Terms terms(float g)
 {
     const float size = fabsf(g);
     Terms t;
-    if (act == ZERO_FFN_GELU) {
+    if constexpr (ACT == ZERO_FFN_GELU) {
         // p = erfc(-g / sqrt 2) / 2, within 32 units and 1.5 g^2 of its argument's
         const float p = 0.5f * erfcf(g * -0.70710678f), bell = 0.39894228f * __builtin_amdgcn_exp2f(g * g * -0.72134752f);
         t.f = g * p;
         t.d = fmaf(g, bell, p);
-        t.slack_f = (40.0f + 2.0f * g * g) * kUnit;
-        t.slack_d = fmaf(size, bell, p) * (44.0f + 2.0f * g * g) * kUnit;
+        t.slack_f = fmaf(g * g, 2.0f * kUnit, 40.0f * kUnit);
+        t.slack_d = fmaf(size, bell, p) * fmaf(g * g, 2.0f * kUnit, 44.0f * kUnit);
         t.sure = size < 12.0f;
         return t;
     }
-    float z = g, dz = 1.0f;  // act(g) = g logistic(z)
-    if (act == ZERO_FFN_GELU_TANH) {
+    float z = g, steep = g;  // act(g) = g logistic(z), steep = g z'
+    if constexpr (ACT == ZERO_FFN_GELU_TANH) {
         z = 1.59576912f * fmaf(0.044715f * g * g, g, g);
-        dz = fmaf(0.214064449f * g, g, 1.59576912f);
+        steep = g * fmaf(0.214064449f * g, g, 1.59576912f);
     }
-    const float e = __builtin_amdgcn_exp2f(z * -1.44269504f), p = __builtin_amdgcn_rcpf(1.0f + e), q = e * p;
-    const float steep = g * dz * q;
+    const float e = __builtin_amdgcn_exp2f(z * -1.44269504f), p = __builtin_amdgcn_rcpf(1.0f + e);
+    const float pull = steep * (e * p);
     t.f = g * p;
-    t.d = fmaf(p, steep, p);
-    // z itself is within 5 units of the exact one
-    const float of_z = act == ZERO_FFN_SILU ? 1.5f * size : 7.0f * fabsf(z);
-    t.slack_f = (8.0f + of_z) * kUnit;
-    t.slack_d = fmaf(p, fabsf(steep), p) * (24.0f + 3.0f * of_z) * kUnit;
+    t.d = fmaf(p, pull, p);
+    // (z itself is within 5 units of the exact one)
+    constexpr float kOfZ = ACT == ZERO_FFN_SILU ? 1.5f * kUnit : 7.0f * kUnit;
+    t.slack_f = fmaf(fabsf(z), kOfZ, 8.0f * kUnit);
+    t.slack_d = fmaf(p, fabsf(pull), p) * fmaf(fabsf(z), 3.0f * kOfZ, 24.0f * kUnit);
     t.sure = fabsf(z) < 80.0f;
     return t;
 }
 
 // The same in fp64.
-__device__ __forceinline__ void terms64(int act, double g, double& f, double& d)
+template <int ACT>
+__device__ __forceinline__ void terms64(double g, double& f, double& d)
 {
-    if (act == ZERO_FFN_GELU) {
+    if constexpr (ACT == ZERO_FFN_GELU) {
         const double p = 0.5 * erfc(g * -0.70710678118654752);
         f = g * p;
         d = fma(g, 0.39894228040143268 * exp(-0.5 * g * g), p);
         return;
     }
-    double z = g, dz = 1.0;
-    if (act == ZERO_FFN_GELU_TANH) {
+    double z = g, steep = g;
+    if constexpr (ACT == ZERO_FFN_GELU_TANH) {
         z = 1.5957691216057308 * (g + 0.044715 * g * g * g);
-        dz = 1.5957691216057308 * (1.0 + 0.134145 * g * g);
+        steep = 1.5957691216057308 * g * (1.0 + 0.134145 * g * g);
     }
-    const double p = 1.0 / (1.0 + exp(-z)), q = 1.0 / (1.0 + exp(z));
+    // p = 1 / (1 + e) and q = 1 - p = e / (1 + e) of e = exp(-|z|), or the other way round
+    const double e = exp(-fabs(z)), big = 1.0 / (1.0 + e), small = e * big;
+    const double p = z < 0.0 ? small : big, q = z < 0.0 ? big : small;
     f = g * p;
-    d = fma(p, g * dz * q, p);
+    d = fma(p, steep * q, p);
 }
 
 // The fp32 value whose rounding to bf16 is that of x.
@@ -84,15 +88,7 @@ __device__ __forceinline__ float for_bf16(double x)
     return __uint_as_float(fabs(static_cast<double>(f)) > fabs(x) ? bits - 1 : bits + 1);
 }
 
-// Whether v, known within slack, has one bf16 value. A zero is exact, and what
-// is so small that fp32's own steps count is not known.
-__device__ __forceinline__ bool open(float v, float slack)
-{
-    const uint32_t both = pack_bf16(v - slack, v + slack);
-    return (both & 0xFFFFu) != both >> 16 || (fabsf(v) < 0x1p-100f && v != 0.0f);
-}
-
-template <bool CODED>
+template <int ACT, bool CODED>
 __global__ __launch_bounds__(kThreads) void ffn_act_grad_kernel(FfnActArgs a, int64_t total, uint32_t nv, FastDiv by_nv)
 {
     // a workgroup's vectors from its first row on: 32 bits are enough
@@ -125,16 +121,23 @@ __global__ __launch_bounds__(kThreads) void ffn_act_grad_kernel(FfnActArgs a, in
     }
     unpack<false>(raw_da, 8 * v, n, da);
     float dg[8], du[8], again[8];
-    uint32_t unsure = 0;
+    uint32_t unsure = 0, least = ~0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const Terms t = terms(a.act, g[i]);
+        const Terms t = terms<ACT>(g[i]);
         const float both = da[i] * u[i];
         dg[i] = both * t.d;
         du[i] = da[i] * t.f;
         again[i] = t.f * u[i];
-        if (!t.sure || open(dg[i], fabsf(both) * t.slack_d) || open(du[i], fabsf(du[i]) * t.slack_f)) unsure |= 1u << i;
+        // both rounded from either end of what they may be (a zero has no slack: it is exact)
+        const float sg = fabsf(both) * t.slack_d, su = fabsf(du[i]) * t.slack_f;
+        const bool apart = pack_bf16(dg[i] - sg, du[i] - su) != pack_bf16(dg[i] + sg, du[i] + su);
+        unsure |= apart || !t.sure ? 1u << i : 0u;
+        // twice the bits without the sign, less one: zeros come last
+        least = min(least, min((__float_as_uint(dg[i]) << 1) - 1, (__float_as_uint(du[i]) << 1) - 1));
     }
+    // Beside values of so little size fp32's smallest steps count: below 2^-100.
+    if (least < 27u << 24) unsure = 0xFF;
     unsure &= (1u << max(n, 0)) - 1;
     while (unsure != 0) {  // of each lane the first one that is left
         const int i = __builtin_ctz(unsure);
@@ -147,7 +150,7 @@ __global__ __launch_bounds__(kThreads) void ffn_act_grad_kernel(FfnActArgs a, in
             di = i == k ? da[k] : di;
         }
         double f, d;
-        terms64(a.act, gi, f, d);
+        terms64<ACT>(gi, f, d);
         const float x = for_bf16(static_cast<double>(di) * ui * d), y = for_bf16(di * f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -168,13 +171,21 @@ __global__ __launch_bounds__(kThreads) void ffn_act_grad_kernel(FfnActArgs a, in
 
 }  // namespace
 
-hipError_t launch_ffn_act_grad(const FfnActArgs& a, hipStream_t s)
+template <int ACT>
+static void launch_act(const FfnActArgs& a, hipStream_t s)
 {
     const uint32_t nv = static_cast<uint32_t>(act8_pitch(a.hidden) / 8);
     const int64_t total = a.rows * nv;
     const unsigned grid = static_cast<unsigned>((total + kThreads - 1) / kThreads);
-    if (a.ckpt[0] != nullptr) ffn_act_grad_kernel<true><<<grid, kThreads, 0, s>>>(a, total, nv, fast_div(nv));
-    else ffn_act_grad_kernel<false><<<grid, kThreads, 0, s>>>(a, total, nv, fast_div(nv));
+    if (a.ckpt[0] != nullptr) ffn_act_grad_kernel<ACT, true><<<grid, kThreads, 0, s>>>(a, total, nv, fast_div(nv));
+    else ffn_act_grad_kernel<ACT, false><<<grid, kThreads, 0, s>>>(a, total, nv, fast_div(nv));
+}
+
+hipError_t launch_ffn_act_grad(const FfnActArgs& a, hipStream_t s)
+{
+    if (a.act == ZERO_FFN_SILU) launch_act<ZERO_FFN_SILU>(a, s);
+    else if (a.act == ZERO_FFN_GELU) launch_act<ZERO_FFN_GELU>(a, s);
+    else launch_act<ZERO_FFN_GELU_TANH>(a, s);
     return hipGetLastError();
 }
 
