@@ -749,59 +749,61 @@ hipError_t launch_tile(const FfnArgs& a, const FfnPlan& plan, hipStream_t s)
     return hipGetLastError();
 }
 
-// A tile shape, the time of a step of one of its workgroups alone on its
-// compute unit, and that of a step of as many as the chip holds at once, us.
+// A tile shape; the time of a step of one of its workgroups alone on its
+// compute unit, of a step of as many as the chip holds at once, and of a round's
+// start and results, us.
 struct Candidate {
     int tile, bm, bn, slots;
-    double alone, full;
+    double alone, full, start;
 };
 template <class T>
-constexpr Candidate candidate(int tile, double alone, double full)
+constexpr Candidate candidate(int tile, double alone, double full, double start)
 {
-    return Candidate{tile, T::BM, T::BN, T::SLOTS, alone, full};
+    return Candidate{tile, T::BM, T::BN, T::SLOTS, alone, full, start};
 }
 enum TileId { kBig, kMid, kSmall, kFlat, kSlow };
 
-FfnPlan plan_for(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t hidden)
+// f(plan, the time that it is expected to take) for every plan of a product.
+template <class F>
+void each_plan(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t hidden, F&& f)
 {
-    static const Candidate kTiles[] = {candidate<Flat>(kFlat, 0.60, 3.3), candidate<Small>(kSmall, 0.70, 1.3),
-                                       candidate<Mid>(kMid, 0.85, 1.2), candidate<Big<kFfnForward>>(kBig, 1.6, 1.7)};
-    static const Candidate kSlowTile = candidate<Slow>(kSlow, 1.5, 2.0);
-    constexpr double kStart = 4.0, kJoin = 5.0, kBytes = 2e6;  // us a round, us a join, bytes of parts written and read a us
-    constexpr int64_t kMostParts = int64_t{1} << 16;           // tiles of one join (its grid's second size)
+    static const Candidate kTiles[] = {candidate<Flat>(kFlat, 0.18, 0.52, 3.0), candidate<Small>(kSmall, 0.17, 0.60, 3.0),
+                                       candidate<Mid>(kMid, 0.25, 0.52, 4.0), candidate<Big<kFfnForward>>(kBig, 0.60, 0.76, 9.0)};
+    static const Candidate kSlowTile = candidate<Slow>(kSlow, 0.60, 1.0, 4.0);
+    constexpr double kJoin = 4.0, kParts = 6e6, kMemory = 5.5e6;  // us a join; bytes a us of parts written and read, and of factors
+    constexpr int64_t kMostParts = int64_t{1} << 16;              // tiles of one join (its grid's second size)
     const int64_t m = kind == kFfnWeight ? hidden : rows, n = kind == kFfnForward ? 2 * hidden : cols;
     const int64_t k = kind == kFfnForward ? cols : kind == kFfnInput ? hidden : rows;
     const int64_t all_steps = (k + BK - 1) / BK * (kind == kFfnInput ? 2 : 1);
-    FfnPlan best{};
-    double least = -1.0;
     const auto consider = [&](const Candidate& c) {
-        const int64_t tiles = (m + c.bm - 1) / c.bm * ((n + c.bn - 1) / c.bn) * (kind == kFfnWeight ? 2 : 1);
-        const int64_t slots = static_cast<int64_t>(c.slots) * kComputeUnits;
-        const auto rounds = [&](int64_t groups, int64_t steps) {
-            const int64_t full = groups / slots, more = groups % slots;
-            const auto step = [&](double fill) { return fill * c.full > c.alone ? fill * c.full : c.alone; };
-            return static_cast<double>(full) * (kStart + static_cast<double>(steps) * step(1.0)) +
-                   (more > 0 ? kStart + static_cast<double>(steps) * step(static_cast<double>(more) / static_cast<double>(slots)) : 0.0);
+        const int64_t tiles_m = (m + c.bm - 1) / c.bm * (kind == kFfnWeight ? 2 : 1), tiles_n = (n + c.bn - 1) / c.bn;
+        const int64_t tiles = tiles_m * tiles_n, slots = static_cast<int64_t>(c.slots) * kComputeUnits;
+        // What one workgroup's step brings from memory: of what it shares with each of its neighbours a third is there.
+        const auto shared = [](int64_t tiles, int64_t most) { return 1.0 + 0.3 * static_cast<double>((tiles < most ? tiles : most) - 1); };
+        const double bytes = 2.0 * BK * (c.bn / shared(tiles_m, 8) + c.bm / shared(tiles_n, 4));
+        // the four waves of the largest backward tile take longer over their results
+        const double start = c.tile == kBig && kind != kFfnForward ? 14.0 : c.start;
+        const auto round = [&](int64_t groups, int64_t steps) {
+            const double g = static_cast<double>(groups), full = g / static_cast<double>(slots) * c.full, memory = g * bytes / kMemory;
+            const double step = full > memory ? full : memory;
+            return start + static_cast<double>(steps) * (step > c.alone ? step : c.alone);
         };
-        const double unsplit = rounds(tiles, all_steps);
-        if (least < 0.0 || unsplit < least) {
-            least = unsplit;
-            best = FfnPlan{c.tile, tiles, 1, all_steps, 0};
-        }
+        const auto rounds = [&](int64_t groups, int64_t steps) {
+            return static_cast<double>(groups / slots) * round(slots, steps) + (groups % slots > 0 ? round(groups % slots, steps) : 0.0);
+        };
+        f(FfnPlan{c.tile, tiles, 1, all_steps, 0}, rounds(tiles, all_steps));
         const int64_t full_rounds = tiles / slots * slots;
         for (const int64_t whole : {int64_t{0}, full_rounds}) {
             const int64_t rest = tiles - whole;
             if (rest == 0 || rest >= kMostParts || (whole == 0 && rest > 2 * slots)) continue;
             for (const int want : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
-                if (all_steps < 2 * want) break;
+                if (all_steps < 4 * want) break;
                 const int64_t steps = (all_steps + want - 1) / want;
                 const int64_t split = (all_steps + steps - 1) / steps;
-                const double bytes = 4.0 * static_cast<double>(rest * split) * c.bm * c.bn;
-                const double us = (whole > 0 ? rounds(whole, all_steps) : 0.0) + rounds(rest * split, steps) + kJoin + bytes / kBytes;
-                if (us < least) {
-                    least = us;
-                    best = FfnPlan{c.tile, whole, static_cast<int>(split), steps, static_cast<size_t>(bytes)};
-                }
+                const double room = 4.0 * static_cast<double>(rest * split) * c.bm * c.bn;
+                const double used = room * static_cast<double>(m < c.bm ? m : c.bm) / c.bm;  // rows beyond the last are not written
+                f(FfnPlan{c.tile, whole, static_cast<int>(split), steps, static_cast<size_t>(room)},
+                  (whole > 0 ? rounds(whole, all_steps) : 0.0) + rounds(rest * split, steps) + kJoin + used / kParts);
             }
             if (full_rounds == 0) break;
         }
@@ -810,6 +812,23 @@ FfnPlan plan_for(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t
     else
         for (const Candidate& c : kTiles)
             if (kind != kFfnWeight || c.bm >= 128) consider(c);
+}
+
+// The plan that is expected to take the least time: rounds of workgroups
+// through the chip, each a start and its steps, and for split tiles their parts
+// written, read and joined by a second launch. Either no tile is whole, or as
+// many as fill whole rounds, or all. The model knows little of what the caches
+// hold; it only has to order the plans.
+FfnPlan plan_for(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t hidden)
+{
+    FfnPlan best{};
+    double least = -1.0;
+    each_plan(kind, aligned, rows, cols, hidden, [&](const FfnPlan& p, double us) {
+        if (least < 0.0 || us < least) {
+            least = us;
+            best = p;
+        }
+    });
     return best;
 }
 
