@@ -177,7 +177,8 @@ enum FfnKind {
 };
 
 // Workspace of a product: the parts of tiles that are split over the summed
-// index, whatever the operands' alignment.
+// index, whatever the operands' alignment, and whether one or both weight
+// gradients are made.
 size_t ffn_workspace_bytes(FfnKind kind, int64_t rows, int64_t cols, int64_t hidden);
 
 struct FfnArgs {
@@ -186,9 +187,9 @@ struct FfnArgs {
     int64_t ld_h;
     const uint16_t* w[2];  // w_gate, w_up
     int64_t ld_w[2];
-    const uint16_t* d[2];  // dgate, dup
+    const uint16_t* d[2];  // dgate, dup; for one weight gradient the first is what it is taken from
     int64_t ld_d[2];
-    Rows out[2];           // gate and up, or dh, or dw_gate and dw_up; p null: not wanted
+    Rows out[2];           // gate and up (p null: not wanted), or dh, or one or two weight gradients
     Rows a;
     uint8_t* ckpt[2];      // of gate and up, or null
     int format;
@@ -196,6 +197,7 @@ struct FfnArgs {
     int accumulate;
     float* part;
     // set at the launch
+    int outputs;    // weight gradients made at once
     int plain;      // whole steps of unaligned operands are read at 32-bit offsets
     int64_t chunk;  // steps of a range of a split tile
     int split;

@@ -513,6 +513,12 @@ int zero_block_ffn_grad(const zero_block_ffn_grad_args* g, void* ws, size_t ws_b
         a.ld_h = g->h.ld;
         a.out[0] = view(g->dw_gate);
         a.out[1] = view(g->dw_up);
+        if (!given(g->dw_gate)) {  // one gradient is the first
+            a.d[0] = a.d[1];
+            a.ld_d[0] = a.ld_d[1];
+            a.out[0] = a.out[1];
+            a.out[1] = Rows{};
+        }
         return hip_status(launch_ffn(kFfnWeight, a, stream));
     }
     for (const bool up : {false, true}) {

@@ -284,8 +284,7 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
     const int part = parted ? id / rest : 0;
     const int split_tile = id - part * rest;  // among the split ones
     const TilePlace place = tile_place(parted ? whole + split_tile : id, tiles_m, tiles_n);
-    const int which = KIND == kFfnWeight && place.m >= tiles_m / 2 ? 1 : 0;
-    if (KIND == kFfnWeight && a.out[which].p == nullptr) return;
+    const int which = KIND == kFfnWeight && a.outputs == 2 && place.m >= tiles_m / 2 ? 1 : 0;
     const int64_t m0 = static_cast<int64_t>(place.m - which * (tiles_m / 2)) * T::BM, n0 = static_cast<int64_t>(place.n) * S::kCols;
     const int64_t m_end = S::m(a), n_end = S::n(a), k_end = S::k(a);
     const int64_t seg_steps = (k_end + BK - 1) / BK;
@@ -654,11 +653,10 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(FfnArgs a, int tiles_m, i
     constexpr int kVecs = S::kCols / 8;
     const int tile = blockIdx.y, vector = blockIdx.x * 256 + threadIdx.x;
     const TilePlace place = tile_place(whole + tile, tiles_m, tiles_n);
-    const int which = KIND == kFfnWeight && place.m >= tiles_m / 2 ? 1 : 0;
+    const int which = KIND == kFfnWeight && a.outputs == 2 && place.m >= tiles_m / 2 ? 1 : 0;
     const int row = vector / kVecs, col = vector % kVecs * 8;
     const int64_t m = static_cast<int64_t>(place.m - which * (tiles_m / 2)) * T::BM + row, n = static_cast<int64_t>(place.n) * S::kCols + col;
     if (m >= S::m(a)) return;  // whole rows
-    if (KIND == kFfnWeight && a.out[which].p == nullptr) return;
     const float* p = a.part + static_cast<int64_t>(tile) * a.split * (T::BM * T::BN) + row * T::BN + col;
     f32x4 s[4] = {};
     for (int k = 0; k < a.split; k += 4) {
@@ -716,7 +714,7 @@ template <FfnKind KIND>
 bool fast(const FfnArgs& a)
 {
     const auto on_16 = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * 2) % 16 == 0; };
-    const bool h = on_16(a.h, a.ld_h), d = on_16(a.d[0], a.ld_d[0]) && on_16(a.d[1], a.ld_d[1]);
+    const bool h = on_16(a.h, a.ld_h), d = on_16(a.d[0], a.ld_d[0]) && ((KIND == kFfnWeight && a.outputs == 1) || on_16(a.d[1], a.ld_d[1]));
     const bool w = on_16(a.w[0], a.ld_w[0]) && on_16(a.w[1], a.ld_w[1]);
     if (!plain<KIND>(a) || a.cols % 8 != 0) return false;
     if (KIND == kFfnForward) return h && w;
@@ -738,7 +736,7 @@ template <class T, FfnKind KIND, bool FAST>
 hipError_t launch_tile(const FfnArgs& a, const FfnPlan& plan, hipStream_t s)
 {
     using S = Shape<T, KIND>;
-    const int m = static_cast<int>((S::m(a) + T::BM - 1) / T::BM) * (KIND == kFfnWeight ? 2 : 1);
+    const int m = static_cast<int>((S::m(a) + T::BM - 1) / T::BM) * a.outputs;
     const int n = static_cast<int>((S::n(a) + S::kCols - 1) / S::kCols);
     const int whole = static_cast<int>(plan.whole), rest = m * n - whole;
     const unsigned grid = static_cast<unsigned>((whole + 7) / 8 * 8 + (static_cast<int64_t>(rest) * plan.split + 7) / 8 * 8);
@@ -765,7 +763,7 @@ enum TileId { kBig, kMid, kSmall, kFlat, kSlow };
 
 // f(plan, the time that it is expected to take) for every plan of a product.
 template <class F>
-void each_plan(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t hidden, F&& f)
+void each_plan(FfnKind kind, bool aligned, int outputs, int64_t rows, int64_t cols, int64_t hidden, F&& f)
 {
     static const Candidate kTiles[] = {candidate<Flat>(kFlat, 0.18, 0.52, 3.0), candidate<Small>(kSmall, 0.17, 0.60, 3.0),
                                        candidate<Mid>(kMid, 0.25, 0.52, 4.0), candidate<Big<kFfnForward>>(kBig, 0.60, 0.76, 9.0)};
@@ -776,7 +774,7 @@ void each_plan(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t h
     const int64_t k = kind == kFfnForward ? cols : kind == kFfnInput ? hidden : rows;
     const int64_t all_steps = (k + BK - 1) / BK * (kind == kFfnInput ? 2 : 1);
     const auto consider = [&](const Candidate& c) {
-        const int64_t tiles_m = (m + c.bm - 1) / c.bm * (kind == kFfnWeight ? 2 : 1), tiles_n = (n + c.bn - 1) / c.bn;
+        const int64_t tiles_m = (m + c.bm - 1) / c.bm * outputs, tiles_n = (n + c.bn - 1) / c.bn;
         const int64_t tiles = tiles_m * tiles_n, slots = static_cast<int64_t>(c.slots) * kComputeUnits;
         // What one workgroup's step brings from memory: of what it shares with each of its neighbours a third is there.
         const auto shared = [](int64_t tiles, int64_t most) { return 1.0 + 0.3 * static_cast<double>((tiles < most ? tiles : most) - 1); };
@@ -819,11 +817,11 @@ void each_plan(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t h
 // written, read and joined by a second launch. Either no tile is whole, or as
 // many as fill whole rounds, or all. The model knows little of what the caches
 // hold; it only has to order the plans.
-FfnPlan plan_for(FfnKind kind, bool aligned, int64_t rows, int64_t cols, int64_t hidden)
+FfnPlan plan_for(FfnKind kind, bool aligned, int outputs, int64_t rows, int64_t cols, int64_t hidden)
 {
     FfnPlan best{};
     double least = -1.0;
-    each_plan(kind, aligned, rows, cols, hidden, [&](const FfnPlan& p, double us) {
+    each_plan(kind, aligned, outputs, rows, cols, hidden, [&](const FfnPlan& p, double us) {
         if (least < 0.0 || us < least) {
             least = us;
             best = p;
@@ -836,8 +834,9 @@ template <FfnKind KIND>
 hipError_t launch_kind(FfnArgs a, hipStream_t s)
 {
     a.plain = plain<KIND>(a);
+    a.outputs = KIND == kFfnWeight && a.out[1].p != nullptr ? 2 : 1;
     const bool aligned = fast<KIND>(a);
-    const FfnPlan plan = plan_for(KIND, aligned, a.rows, a.cols, a.hidden);
+    const FfnPlan plan = plan_for(KIND, aligned, a.outputs, a.rows, a.cols, a.hidden);
     a.chunk = plan.chunk;
     a.split = plan.split;
     switch (plan.tile) {
@@ -857,8 +856,13 @@ hipError_t launch_kind(FfnArgs a, hipStream_t s)
 
 size_t ffn_workspace_bytes(FfnKind kind, int64_t rows, int64_t cols, int64_t hidden)
 {
-    const size_t aligned = plan_for(kind, true, rows, cols, hidden).bytes, slow = plan_for(kind, false, rows, cols, hidden).bytes;
-    return aligned > slow ? aligned : slow;
+    size_t most = 0;
+    for (const bool aligned : {true, false})
+        for (int outputs = 1; outputs <= (kind == kFfnWeight ? 2 : 1); ++outputs) {
+            const size_t bytes = plan_for(kind, aligned, outputs, rows, cols, hidden).bytes;
+            if (bytes > most) most = bytes;
+        }
+    return most;
 }
 
 hipError_t launch_ffn(FfnKind kind, const FfnArgs& a, hipStream_t s)

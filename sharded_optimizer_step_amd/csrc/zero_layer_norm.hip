@@ -12,9 +12,10 @@ namespace {
 // How many columns lie in the row from vector v on.
 __device__ __forceinline__ int columns(int cols, int v, int nv) { return v < nv ? cols - 8 * v : 0; }
 
-// A row's mean in two parts and its reciprocal root.
+// A row's mean and its reciprocal root, in two parts each.
 struct Moments {
-    float mean, lo, rstd;
+    float mean, lo;
+    Rstd rstd;
 };
 
 // The moments of a row from what its lanes hold. A wave takes a first mean m of
@@ -86,7 +87,7 @@ __device__ __forceinline__ Moments moments(float (&x)[V][8], int lane, int lanes
     out.mean = first + step;
     out.lo = (first - out.mean) + step;
     // all columns alike may leave less than nothing
-    out.rstd = row_rstd(squares < 0.0f ? 0.0f : squares, inv_cols, eps).hi;
+    out.rstd = row_rstd(squares < 0.0f ? 0.0f : squares, inv_cols, eps);
     return out;
 }
 
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void layer_norm_kernel(Laye
         const Moments m = moments<WAVE, V>(x, lane, lanes, a.cols, nv, inv_cols, a.eps, red, half);
         if (lane == 0) {
             if (a.mean != nullptr) ((ZERO_G float*)a.mean)[row] = m.mean;
-            if (a.rstd != nullptr) ((ZERO_G float*)a.rstd)[row] = m.rstd;
+            if (a.rstd != nullptr) ((ZERO_G float*)a.rstd)[row] = m.rstd.hi;
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -168,7 +169,10 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxLanes) void layer_norm_kernel(Laye
             float xn[8], h[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                xn[i] = i < n ? ((x[j][i] - m.mean) - m.lo) * m.rstd : 0.0f;
+                // the difference and the root in two parts: rounded once, so that its 8-bit code is seldom another
+                const float c = x[j][i] - m.mean, rest = ((x[j][i] - c) - m.mean) - m.lo;
+                const float q = fmaf(c, m.rstd.hi, fmaf(c, m.rstd.lo, rest * m.rstd.hi));
+                xn[i] = i < n ? q : 0.0f;
                 h[i] = fmaf(w[i], xn[i], b[i]);
             }
             if (a.ckpt_xn != nullptr) save8(a.ckpt_xn, a.rows, pitch, a.format, row, v, xn);

@@ -92,7 +92,7 @@ def test_forward(rows, cols, hidden, pad, offset):
         check_forward(b, place, (act, saved))
 
 
-@pytest.mark.parametrize("rows,cols,hidden", [(2000, 512, 4500), (4200, 264, 2200)])
+@pytest.mark.parametrize("rows,cols,hidden", [(2000, 512, 4500), (4200, 264, 2200), (1100, 776, 2048), (4096, 2056, 4360), (50, 4096, 5000)])
 def test_forward_of_large_tiles(rows, cols, hidden):
     for saved in ("raw", "8bit"):
         check_forward(*forward(rows, cols, hidden, saved=saved, act="gelu_tanh", fmt="int8"))
@@ -205,7 +205,8 @@ def test_backward(rows, cols, hidden, pad, offset):
         check_backward(*r, (act, saved, inp))
 
 
-@pytest.mark.parametrize("rows,cols,hidden", [(2000, 2104, 1544), (1100, 1000, 5000), (5000, 72, 136)])
+@pytest.mark.parametrize("rows,cols,hidden", [(2000, 2104, 1544), (1100, 1000, 5000), (5000, 72, 136), (3000, 2304, 4360), (700, 4096, 3000),
+                                              (4099, 776, 2056), (50, 2048, 6000)])
 def test_backward_of_large_tiles(rows, cols, hidden):
     check_backward(*backward(rows, cols, hidden, act="gelu_tanh", halves=True, again=True))
     check_backward(*backward(rows, cols, hidden, saved="raw", grad=BF16, accumulate=False))
@@ -215,6 +216,54 @@ def test_backward_of_large_tiles(rows, cols, hidden):
 @pytest.mark.parametrize("inp,scale", [("raw", False), ("8bit", True), ("8bit", False)])
 def test_backward_operands(dh, dw, inp, scale):
     check_backward(*backward(70, 90, 110, dh=dh, dw=dw, input=inp, scale=scale, again=True, fmt="int8"))
+
+
+def test_operands_with_strides_of_their_own():
+    """Weights and gradients whose two halves lie differently: no common offsets, and one of them unaligned."""
+    for other in (16, 3):
+        r = backward(300, 264, 520, saved="raw", accumulate=False)
+        b, place = r[0], Placed(other, 0)
+        b.w_up, b.dup, b.dw_up = place(b.w_up), place(b.dup), place(b.dw_up)
+        z.zero_block_ffn_grad(b, 0, z.workspace(z.zero_block_ffn_grad_workspace_bytes(300, 264, 520)))
+        check_backward(b, place, *r[2:])
+        f, place = forward(300, 264, 520)
+        own = Placed(other, 0)
+        f.w_up, f.up = own(f.w_up), own(f.up)
+        z.zero_block_ffn(f, z.workspace(z.zero_block_ffn_workspace_bytes(300, 264, 520)))
+        check_forward(f, own)
+
+
+def test_rows_far_apart():
+    """Row strides beyond what 32-bit offsets reach over a tile."""
+    ld, g = (1 << 22) + 8, gen(2)
+    wide = torch.zeros(40, ld, dtype=BF16, device="cuda")
+    h = wide[:, :72]
+    h.copy_(rnd(g, 40, 72))
+    f = z.BlockFfn(h=h, w_gate=rnd(g, 96, 72, scale=0.1), w_up=rnd(g, 96, 72, scale=0.1), a=torch.zeros(40, 96, dtype=BF16, device="cuda"))
+    z.zero_block_ffn(f, z.workspace(z.zero_block_ffn_workspace_bytes(40, 72, 96)))
+    check_forward(f, Placed(0, 0))
+    dw = torch.zeros(96, 72, device="cuda")
+    b = z.BlockFfnGrad(da=rnd(g, 40, 96), dgate=torch.zeros(40, 96, dtype=BF16, device="cuda"), dup=torch.zeros(40, 96, dtype=BF16, device="cuda"),
+                       gate=rnd(g, 40, 96), up=rnd(g, 40, 96), h=h, dw_gate=dw)
+    z.zero_block_ffn_grad(b, 0, z.workspace(z.zero_block_ffn_grad_workspace_bytes(40, 72, 96)))
+    check_backward(b, Placed(0, 0), b.gate.double(), b.up.double(), h.double(), dict(dw_gate=torch.zeros_like(dw).double()))
+
+
+def test_tensors_of_more_than_32_bits_of_bytes():
+    """The last rows of operands of 4.3 GB and more."""
+    rows, cols, hidden, g = (1 << 17) + 5, 64, 16640, gen(7)
+    last = slice(rows - 5, rows)
+    f = z.BlockFfn(h=rnd(g, rows, cols), w_gate=rnd(g, hidden, cols, scale=0.125), w_up=rnd(g, hidden, cols, scale=0.125),
+                   a=torch.zeros(rows, hidden, dtype=BF16, device="cuda"), gate=torch.zeros(rows, hidden, dtype=BF16, device="cuda"))
+    assert f.a.numel() * 2 > 1 << 32
+    z.zero_block_ffn(f, z.workspace(z.zero_block_ffn_workspace_bytes(rows, cols, hidden)))
+    few = z.BlockFfn(h=f.h[last], w_gate=f.w_gate, w_up=f.w_up, a=f.a[last], gate=f.gate[last])
+    check_forward(few, Placed(0, 0))
+    b = z.BlockFfnGrad(da=f.a, dgate=torch.zeros_like(f.a), dup=torch.zeros_like(f.a), gate=f.gate, up=f.gate, w_gate=f.w_gate, w_up=f.w_up,
+                       dh=torch.zeros_like(f.h))
+    z.zero_block_ffn_grad(b, 0, z.workspace(z.zero_block_ffn_grad_workspace_bytes(rows, cols, hidden)))
+    few = z.BlockFfnGrad(da=b.da[last], dgate=b.dgate[last], dup=b.dup[last], w_gate=b.w_gate, w_up=b.w_up, dh=b.dh[last])
+    check_backward(few, Placed(0, 0), f.gate[last].double(), f.gate[last].double(), None, {})
 
 
 def test_backward_of_empty_sizes():
