@@ -769,11 +769,17 @@ void each_plan(FfnKind kind, bool aligned, int outputs, int64_t rows, int64_t co
                                        candidate<Mid>(kMid, 0.25, 0.52, 4.0), candidate<Big<kFfnForward>>(kBig, 0.60, 0.76, 9.0)};
     static const Candidate kSlowTile = candidate<Slow>(kSlow, 0.60, 1.0, 4.0);
     constexpr double kJoin = 4.0, kParts = 6e6, kMemory = 5.5e6;  // us a join; bytes a us of parts written and read, and of factors
+    constexpr double kCaches = 64e6;                              // bytes of factors: twice the L2s
     constexpr int64_t kMostParts = int64_t{1} << 16;              // tiles of one join (its grid's second size)
     const int64_t m = kind == kFfnWeight ? hidden : rows, n = kind == kFfnForward ? 2 * hidden : cols;
     const int64_t k = kind == kFfnForward ? cols : kind == kFfnInput ? hidden : rows;
     const int64_t all_steps = (k + BK - 1) / BK * (kind == kFfnInput ? 2 : 1);
+    // A workgroup alone waits longer for a step that comes from memory than for one that the L2s hold: with one
+    // time for both, dh of 128 rows x 4096 x 11008 from memory took 84 us and now 63, or that of 4096 rows x 768 x
+    // 2048 41 instead of 33.
+    const double far = 2.0 * static_cast<double>(m + n) * static_cast<double>(k) * (kind == kFfnInput ? 2 : 1) > kCaches ? 1.5 : 1.0;
     const auto consider = [&](const Candidate& c) {
+        const double alone = c.alone * far < c.full ? c.alone * far : c.alone < c.full ? c.full : c.alone;
         const int64_t tiles_m = (m + c.bm - 1) / c.bm * outputs, tiles_n = (n + c.bn - 1) / c.bn;
         const int64_t tiles = tiles_m * tiles_n, slots = static_cast<int64_t>(c.slots) * kComputeUnits;
         // What one workgroup's step brings from memory: of what it shares with each of its neighbours a third is there.
@@ -784,7 +790,7 @@ void each_plan(FfnKind kind, bool aligned, int outputs, int64_t rows, int64_t co
         const auto round = [&](int64_t groups, int64_t steps) {
             const double g = static_cast<double>(groups), full = g / static_cast<double>(slots) * c.full, memory = g * bytes / kMemory;
             const double step = full > memory ? full : memory;
-            return start + static_cast<double>(steps) * (step > c.alone ? step : c.alone);
+            return start + static_cast<double>(steps) * (step > alone ? step : alone);
         };
         const auto rounds = [&](int64_t groups, int64_t steps) {
             return static_cast<double>(groups / slots) * round(slots, steps) + (groups % slots > 0 ? round(groups % slots, steps) : 0.0);
