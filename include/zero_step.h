@@ -930,8 +930,10 @@ typedef struct zero_block_ffn_args {
     int32_t act;      /* ZERO_FFN_* */
 } zero_block_ffn_args;
 
-/* Workspace size of zero_block_ffn (partial sums where few rows leave the
- * chip's units to the summed columns; often 0); 0 on invalid sizes. */
+/* Workspace size of zero_block_ffn: partial sums where few rows leave the
+ * chip's units to the summed columns (often none), and where cols is not a
+ * multiple of 8 and rows are many, aligned copies of h and the weights. 0 on
+ * invalid sizes. */
 size_t zero_block_ffn_workspace_bytes(int64_t rows, int64_t cols, int64_t hidden);
 
 /* ws: as in zero_act8_wgrad. */
@@ -984,7 +986,9 @@ typedef struct zero_block_ffn_grad_args {
 } zero_block_ffn_grad_args;
 
 /* Workspace size of zero_block_ffn_grad, whichever of its gradients are wanted
- * and however h comes; 0 on invalid sizes. */
+ * and however h comes: partial sums, and where cols or hidden is not a multiple
+ * of 8 and rows are many, aligned copies of a product's operands. 0 on invalid
+ * sizes. */
 size_t zero_block_ffn_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t hidden);
 
 /* ws: as in zero_act8_wgrad. */

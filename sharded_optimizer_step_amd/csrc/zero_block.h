@@ -176,9 +176,10 @@ enum FfnKind {
     kFfnWeight,   // dw_gate = dgate^T h and dw_up = dup^T h
 };
 
-// Workspace of a product: the parts of tiles that are split over the summed
-// index, whatever the operands' alignment, and whether one or both weight
-// gradients are made.
+// Workspace of a product: aligned copies of operands whose columns are not a
+// multiple of 8, and the parts of tiles that are split over the summed index,
+// whatever the operands' alignment, and whether one or both weight gradients
+// are made.
 size_t ffn_workspace_bytes(FfnKind kind, int64_t rows, int64_t cols, int64_t hidden);
 
 struct FfnArgs {

@@ -302,13 +302,15 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
     // Rows beyond the last one are read as the last one, columns as the last
     // eight (which is where a unit that ends beyond them lies, moved into place
     // by `shift` elements): products of what is beyond are not stored. Offsets
-    // are from eight elements before a tile, so that none is negative.
+    // are from eight elements before a tile, so that none is negative. (An aligned
+    // factor's rows hold whole units: what a copy has beyond its columns are zeros.)
+    const auto held = [](int64_t columns) { return FAST ? (columns + 7) / 8 * 8 : columns; };
     uint32_t off_a[A::kVecs], off_b[B::kVecs];
 #pragma unroll
     for (int i = 0; i < A::kVecs; ++i) {
         const int64_t ld = KIND == kFfnForward ? a.ld_h : a.ld_d[which];
         const int64_t row = kAlongA ? min(static_cast<int64_t>(row_a + i * A::kStep), m_end - 1 - m0) : row_a + i * A::kStep;
-        const int64_t col = kAlongA ? unit_a(i) * 8 : min(static_cast<int64_t>(unit_a(i) * 8), m_end - 8 - m0);
+        const int64_t col = kAlongA ? unit_a(i) * 8 : min(static_cast<int64_t>(unit_a(i) * 8), held(m_end) - 8 - m0);
         off_a[i] = static_cast<uint32_t>((row * ld + col + 8) * 2);
     }
 #pragma unroll
@@ -316,7 +318,7 @@ __global__ __launch_bounds__(T::NT, T::kWavesASimd) void ffn_kernel(FfnArgs a, i
         const int64_t ld = KIND == kFfnWeight ? a.ld_h : a.ld_w[KIND == kFfnForward && i >= kHalfB ? 1 : 0];
         const int r = row_b + i % kHalfB * B::kStep;
         const int64_t row = kAlongB ? min(static_cast<int64_t>(r), n_end - 1 - n0) : r;
-        const int64_t col = kAlongB ? unit_b(i) * 8 : min(static_cast<int64_t>(unit_b(i) * 8), n_end - 8 - n0);
+        const int64_t col = kAlongB ? unit_b(i) * 8 : min(static_cast<int64_t>(unit_b(i) * 8), held(n_end) - 8 - n0);
         off_b[i] = static_cast<uint32_t>((row * ld + col + 8) * 2);
     }
     const auto shift_of = [](int64_t over) { return over > 0 && over < 8 ? static_cast<int>(over) : 0; };
@@ -709,11 +711,13 @@ bool plain(const FfnArgs& a)
     return d && h && a.hidden >= 8 && a.cols >= 8;
 }
 
+// Every row of an operand starts on 16 bytes.
+bool on_16(const uint16_t* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * 2) % 16 == 0; }
+
 // Whether every 16-byte unit that a product reads also lies on 16 bytes and inside its row.
 template <FfnKind KIND>
 bool fast(const FfnArgs& a)
 {
-    const auto on_16 = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * 2) % 16 == 0; };
     const bool h = on_16(a.h, a.ld_h), d = on_16(a.d[0], a.ld_d[0]) && ((KIND == kFfnWeight && a.outputs == 1) || on_16(a.d[1], a.ld_d[1]));
     const bool w = on_16(a.w[0], a.ld_w[0]) && on_16(a.w[1], a.ld_w[1]);
     if (!plain<KIND>(a) || a.cols % 8 != 0) return false;
@@ -767,7 +771,7 @@ void each_plan(FfnKind kind, bool aligned, int outputs, int64_t rows, int64_t co
 {
     static const Candidate kTiles[] = {candidate<Flat>(kFlat, 0.18, 0.52, 3.0), candidate<Small>(kSmall, 0.17, 0.60, 3.0),
                                        candidate<Mid>(kMid, 0.25, 0.52, 4.0), candidate<Big<kFfnForward>>(kBig, 0.60, 0.76, 9.0)};
-    static const Candidate kSlowTile = candidate<Slow>(kSlow, 0.60, 1.0, 4.0);
+    static const Candidate kSlowTile = candidate<Slow>(kSlow, 0.70, 0.95, 5.0);
     constexpr double kJoin = 4.0, kParts = 6e6, kMemory = 5.5e6;  // us a join; bytes a us of parts written and read, and of factors
     constexpr double kCaches = 64e6;                              // bytes of factors: twice the L2s
     constexpr int64_t kMostParts = int64_t{1} << 16;              // tiles of one join (its grid's second size)
@@ -823,7 +827,11 @@ void each_plan(FfnKind kind, bool aligned, int outputs, int64_t rows, int64_t co
 // written, read and joined by a second launch. Either no tile is whole, or as
 // many as fill whole rounds, or all. The model knows little of what the caches
 // hold; it only has to order the plans.
-FfnPlan plan_for(FfnKind kind, bool aligned, int outputs, int64_t rows, int64_t cols, int64_t hidden)
+struct TimedPlan {
+    FfnPlan plan;
+    double us;
+};
+TimedPlan plan_for(FfnKind kind, bool aligned, int outputs, int64_t rows, int64_t cols, int64_t hidden)
 {
     FfnPlan best{};
     double least = -1.0;
@@ -833,7 +841,107 @@ FfnPlan plan_for(FfnKind kind, bool aligned, int outputs, int64_t rows, int64_t 
             best = p;
         }
     });
-    return best;
+    return TimedPlan{best, least};
+}
+
+// A factor of a product: rows and columns of an operand.
+struct Operand {
+    const uint16_t* p;
+    int64_t ld, rows, cols;
+};
+
+// f(operand) for each of a product's factors.
+template <class F>
+void each_operand(FfnKind kind, FfnArgs& a, int outputs, F&& f)
+{
+    if (kind != kFfnForward) {
+        f(a.d[0], a.ld_d[0], a.rows, a.hidden);
+        if (kind == kFfnInput || outputs == 2) f(a.d[1], a.ld_d[1], a.rows, a.hidden);
+    }
+    if (kind != kFfnInput) f(a.h, a.ld_h, a.rows, a.cols);
+    if (kind != kFfnWeight) {
+        f(a.w[0], a.ld_w[0], a.hidden, a.cols);
+        f(a.w[1], a.ld_w[1], a.hidden, a.cols);
+    }
+}
+
+// Whether a product whose operands' rows do not all hold whole units of 16
+// bytes, because there are not a multiple of 8 columns, copies them to the
+// workspace first, zeros up to whole units, and then takes the tiles that go
+// straight to LDS. Loads at odd addresses take more than twice as long as
+// aligned ones, for every tile that they are part of; a copy reads each
+// operand once. 2011 rows x 1003 x 2731: forward 72 -> 51 us, dh 61 -> 57, both
+// weight gradients 64 -> 46; 4096 x 4091 x 4093: 462 -> 260, 408 -> 251 and 420 ->
+// 225. A few rows do not repay their weights' copy: forward 16 x 1003 x 2731
+// takes 14 us as they are and 18 from copies, 64 x 4091 x 11003 62 and 124. (Operands of a multiple of 8
+// columns that lie at odd addresses or strides are read where they are: a
+// caller can place them better, and the workspace of those who did is smaller.)
+struct CopyPlan {
+    TimedPlan timed;
+    size_t bytes;  // of the copies; 0: none are made
+};
+CopyPlan plan_unaligned(FfnKind kind, int outputs, int64_t rows, int64_t cols, int64_t hidden)
+{
+    const CopyPlan here{plan_for(kind, false, outputs, rows, cols, hidden), 0};
+    if ((cols % 8 == 0 && (kind == kFfnForward || hidden % 8 == 0)) || rows == 0 || cols < 8 || hidden < 8) return here;
+    constexpr double kCopy = 3.0, kCopied = 6e6;  // us a launch; bytes read and written a us
+    size_t bytes = 0;
+    bool fits = true;
+    FfnArgs none{};
+    none.rows = rows;
+    none.cols = cols;
+    none.hidden = hidden;
+    each_operand(kind, none, outputs, [&](const uint16_t*, int64_t, int64_t r, int64_t c) {
+        const int64_t units = (c + 7) / 8;
+        if (c > (int64_t{1} << 22) - 8 || r > (int64_t{1} << 30) / units) fits = false;  // offsets of a tile; units in 32 bits
+        else bytes += (static_cast<size_t>(r * units) * 16 + 255) / 256 * 256;
+    });
+    if (!fits) return here;
+    TimedPlan copied = plan_for(kind, true, outputs, rows, cols, hidden);
+    copied.us += kCopy + 2.0 * static_cast<double>(bytes) / kCopied;
+    return copied.us < here.timed.us ? CopyPlan{copied, bytes} : here;
+}
+
+// Operands, and where their copies lie.
+struct CopyArgs {
+    Operand from[4];
+    uint16_t* to[4];
+    FastDiv units[4];  // of a row
+};
+
+// A thread copies a unit, 8 columns: a stream.
+__global__ __launch_bounds__(256) void ffn_copy_kernel(CopyArgs c)
+{
+    const Operand& o = c.from[blockIdx.y];
+    const uint32_t units = static_cast<uint32_t>((o.cols + 7) / 8), at = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t row = div_by(at, c.units[blockIdx.y]), unit = at - row * units;
+    if (row >= o.rows) return;
+    *(ZERO_G u32x4*)(c.to[blockIdx.y] + static_cast<int64_t>(at) * 8) = load_unit(o.p + row * o.ld, int64_t{unit} * 8, o.cols);
+}
+
+// The operands whose rows do not lie on 16 bytes or end inside a unit, copied to
+// the workspace and so aligned; the parts of split tiles come behind them.
+hipError_t copy_operands(FfnKind kind, FfnArgs& a, size_t bytes, hipStream_t s)
+{
+    CopyArgs c{};
+    int n = 0;
+    int64_t most = 0;
+    char* to = reinterpret_cast<char*>(a.part);
+    a.part = reinterpret_cast<float*>(to + bytes);
+    each_operand(kind, a, a.outputs, [&](const uint16_t*& p, int64_t& ld, int64_t rows, int64_t cols) {
+        if (cols % 8 == 0 && on_16(p, ld)) return;
+        const int64_t units = (cols + 7) / 8;
+        c.from[n] = Operand{p, ld, rows, cols};
+        c.to[n] = reinterpret_cast<uint16_t*>(to);
+        c.units[n] = fast_div(static_cast<uint32_t>(units));
+        ++n;
+        p = reinterpret_cast<const uint16_t*>(to);
+        ld = units * 8;
+        to += (rows * units * 16 + 255) / 256 * 256;
+        if (rows * units > most) most = rows * units;
+    });
+    ffn_copy_kernel<<<dim3(static_cast<unsigned>((most + 255) / 256), static_cast<unsigned>(n)), 256, 0, s>>>(c);
+    return hipGetLastError();
 }
 
 template <FfnKind KIND>
@@ -841,8 +949,17 @@ hipError_t launch_kind(FfnArgs a, hipStream_t s)
 {
     a.plain = plain<KIND>(a);
     a.outputs = KIND == kFfnWeight && a.out[1].p != nullptr ? 2 : 1;
-    const bool aligned = fast<KIND>(a);
-    const FfnPlan plan = plan_for(KIND, aligned, a.outputs, a.rows, a.cols, a.hidden);
+    FfnPlan plan;
+    if (fast<KIND>(a)) {
+        plan = plan_for(KIND, true, a.outputs, a.rows, a.cols, a.hidden).plan;
+    } else {
+        const CopyPlan odd = plan_unaligned(KIND, a.outputs, a.rows, a.cols, a.hidden);
+        plan = odd.timed.plan;
+        if (odd.bytes > 0) {
+            const hipError_t e = copy_operands(KIND, a, odd.bytes, s);
+            if (e != hipSuccess) return e;
+        }
+    }
     a.chunk = plan.chunk;
     a.split = plan.split;
     switch (plan.tile) {
@@ -863,11 +980,11 @@ hipError_t launch_kind(FfnArgs a, hipStream_t s)
 size_t ffn_workspace_bytes(FfnKind kind, int64_t rows, int64_t cols, int64_t hidden)
 {
     size_t most = 0;
-    for (const bool aligned : {true, false})
-        for (int outputs = 1; outputs <= (kind == kFfnWeight ? 2 : 1); ++outputs) {
-            const size_t bytes = plan_for(kind, aligned, outputs, rows, cols, hidden).bytes;
+    for (int outputs = 1; outputs <= (kind == kFfnWeight ? 2 : 1); ++outputs) {
+        const CopyPlan odd = plan_unaligned(kind, outputs, rows, cols, hidden);
+        for (const size_t bytes : {plan_for(kind, true, outputs, rows, cols, hidden).plan.bytes, odd.bytes + odd.timed.plan.bytes})
             if (bytes > most) most = bytes;
-        }
+    }
     return most;
 }
 

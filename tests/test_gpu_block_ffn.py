@@ -389,3 +389,66 @@ def test_captured_graph(rows, cols, hidden):
         z.zero_block_ffn(f, ws)
         z.zero_block_ffn_grad(b, 0, wsb)
         assert all(torch.equal(x, y) for x, y in zip(got, [f.a, f.gate, f.up] + results(b)))
+
+
+# ------------------------------------------------------------------ columns that are no multiple of 8
+
+ODD = [(300, 767, 2049), (640, 767, 1001), (1000, 4093, 1001), (900, 1003, 1024), (900, 72, 2049), (2011, 1003, 2731), (16, 1003, 2731)]
+
+
+def among_nans(t):
+    """t as a view of rows that NaN follow and that lie at odd addresses."""
+    rows, cols = t.shape
+    buf = torch.full((rows * (cols + 5) + 9,), float("nan"), dtype=t.dtype, device="cuda")
+    v = buf[1:1 + rows * (cols + 5)].view(rows, cols + 5)[:, :cols]
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("rows,cols,hidden", ODD)
+def test_what_lies_beyond_the_columns_counts_nothing(rows, cols, hidden):
+    """Operands among NaN, and a workspace full of them."""
+    f, place = forward(rows, cols, hidden)
+    f.h, f.w_gate, f.w_up = among_nans(f.h), among_nans(f.w_gate), among_nans(f.w_up)
+    ws = z.workspace(max(1, z.zero_block_ffn_workspace_bytes(rows, cols, hidden)))
+    ws.fill_(255)
+    z.zero_block_ffn(f, ws)
+    check_forward(f, place)
+    for dw in ("gu", "u"):
+        r = backward(rows, cols, hidden, saved="raw", accumulate=False, dw=dw)
+        b = r[0]
+        for k in ("da", "gate", "up", "h", "w_gate", "w_up"):
+            setattr(b, k, among_nans(getattr(b, k)))
+        b.dgate, b.dup = among_nans(b.dgate), among_nans(b.dup)
+        ws = z.workspace(max(1, z.zero_block_ffn_grad_workspace_bytes(rows, cols, hidden)))
+        ws.fill_(255)
+        z.zero_block_ffn_grad(b, 0, ws)
+        check_backward(*r)
+
+
+def test_odd_columns_in_a_captured_graph():
+    test_captured_graph(640, 767, 1001)
+
+
+def test_an_aligned_call_and_an_odd_one_agree():
+    """One column of zeros more changes no sum."""
+    rows, cols, hidden = 640, 767, 1000
+    f, _ = forward(rows, cols, hidden)
+    wide = lambda t: torch.nn.functional.pad(t, (0, 1))  # noqa: E731
+    g = z.BlockFfn(h=wide(f.h), w_gate=wide(f.w_gate), w_up=wide(f.w_up), a=torch.zeros_like(f.a), act=f.act)
+    z.zero_block_ffn(g, z.workspace(z.zero_block_ffn_workspace_bytes(rows, cols + 1, hidden)))
+    ref = ffn_reference(f)
+    assert_close(g.a, *ref["a"])
+    assert_close(f.a, *ref["a"])
+
+
+# ------------------------------------------------------------------ what is saved
+
+@pytest.mark.parametrize("saved", ["gate", "up", "ckpt_gate", "ckpt_up", "gate ckpt_up", "up ckpt_gate", "gate up ckpt_gate ckpt_up"])
+@pytest.mark.parametrize("rows,cols,hidden", [(5, 100, 130), (257, 192, 257)])
+def test_forward_saves_what_is_asked(rows, cols, hidden, saved):
+    b, place = forward(rows, cols, hidden, saved="none")
+    for k in saved.split():
+        setattr(b, k, z.new_act8(rows, hidden) if "ckpt" in k else torch.zeros(rows, hidden, dtype=BF16, device="cuda"))
+    z.zero_block_ffn(b, z.workspace(z.zero_block_ffn_workspace_bytes(rows, cols, hidden)))
+    check_forward(b, place, saved)

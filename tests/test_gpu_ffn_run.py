@@ -183,6 +183,8 @@ def backward_call(wants, rows, cols, hidden, ws):
 CALLS = [(norm_call, w, c) for c in (512, 8200) for w in ((), ("dw",), ("db",), ("dw", "db"))]
 CALLS += [(forward_call, 8, 20000, 64), (backward_call, ("dh",), 8, 64, 20000)]
 CALLS += [(backward_call, w, 20000, 64, 64) for w in (("dw_gate",), ("dw_up",), ("dw_gate", "dw_up"))]
+# odd columns: copies of the operands
+CALLS += [(forward_call, 640, 767, 1001)] + [(backward_call, w, 640, 767, 1001) for w in (("dh",), ("dw_gate",), ("dw_up",))]
 
 
 @pytest.mark.parametrize("case", CALLS)
