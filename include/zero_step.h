@@ -906,8 +906,9 @@ int zero_layer_norm_grad(const zero_layer_norm_grad_args* args, void* ws, size_t
 
 /*
  * zero_block_ffn -- both projections, the activation and the product in one
- * kernel. gate and up are summed in fp32 in an order that depends only on the
- * sizes, and a is made from these sums. For the backward pass they can be kept
+ * pass. gate and up are summed in fp32 in an order that depends only on the
+ * sizes and on which operands' rows lie on 16 bytes, and a is made from these
+ * sums. For the backward pass they can be kept
  * as bf16 rows (gate, up) or as act8 buffers (ckpt_gate, ckpt_up), or neither;
  * each result is rounded to its own type once. cols == 0: the sums are 0.
  * rows < 2^31, cols and hidden <= 2^30, rows times either (rounded up to 32)
@@ -948,7 +949,8 @@ int zero_block_ffn(const zero_block_ffn_args* args, void* ws, size_t ws_bytes, h
  * dgate and dup are the nearest bf16 values of the formulas (computed in fp32,
  * and in fp64 where that leaves the rounding open); dh and the weight gradients
  * are those of dgate and dup as stored, summed in fp32 in an order that depends
- * only on the sizes, each rounded to its own type once.
+ * only on the sizes, on which of them are wanted and on which operands' rows lie
+ * on 16 bytes, each rounded to its own type once.
  * The block's input comes as bf16 rows h, or as the act8 buffer ckpt_h whose
  * decoded columns are multiplied with col_scale (cols values, bf16 or fp32;
  * absent: ones), as in zero_act8_wgrad. ckpt_a, if given, is written: the act8
