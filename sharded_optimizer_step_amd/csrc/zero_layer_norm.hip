@@ -3,8 +3,8 @@
 //
 // A row stays in the registers of L lanes, V vectors of 8 columns a lane, so
 // every operand is read once and every result written once. Both passes are
-// streams, bound by HBM: 16384 x 4096 forward with x_out and 8 bits saved 115
-// us (606 MB, 5.3 TB/s), backward from 8 bits 92 us (472 MB, 5.1 TB/s) and 5 to
+// streams, bound by HBM: 16384 x 4096 forward with x_out and 8 bits saved 113
+// us (606 MB, 5.4 TB/s), backward from 8 bits 92 us (472 MB, 5.1 TB/s) and 5 to
 // join the column sums; unaligned fp32 rows of 5003, backward, 56 us (240 MB, 4.3
 // TB/s). A short call is bound by its launch: 128 x 768 4.8 us.
 #include "zero_norm_device.h"
