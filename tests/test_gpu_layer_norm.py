@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import sharded_optimizer_step_amd as z
-from block_cases import FORMATS, U, assert_within, canary_ok, decode_act8, strided
+from block_cases import FORMATS, U, assert_within, canary_ok, decode_act8, round_act8, strided
 from ffn_cases import assert_close, assert_saved_within, layer_norm_grad_reference, layer_norm_reference
 
 pytestmark = pytest.mark.gpu
@@ -274,3 +274,47 @@ def test_captured_graph(cols):
         for a, b in zip(got, (n.h, n.mean, n.x_out, g.dx, g.dw, g.db)):
             assert torch.equal(a, b)
         check_forward(n, seed)
+
+
+# bf16 rows, whose first means have 16 bits, and rows of all sizes at once
+@pytest.mark.parametrize("kind", ["far", "one off", "two values", "tiny among large", "all sizes", "equal"])
+@pytest.mark.parametrize("cols", [7, 100, 512, 513, 4096, 5003, 12000])
+def test_bf16_rows_far_from_zero_and_of_all_sizes(cols, kind):
+    g, rows = gen(cols), 17
+    x = rnd(g, rows, cols)
+    if kind == "far":
+        x = x + 300 * torch.arange(1, rows + 1, device="cuda")[:, None]
+    elif kind == "one off":  # the least variance that unequal values have
+        x = torch.full((rows, cols), 255.0, device="cuda")
+        x[:, cols // 2] = 254.0
+    elif kind == "two values":
+        x = 1000 + 8 * (x > 0).float()
+    elif kind == "tiny among large":
+        x = torch.where(x > 1, 1e-6 * x, 77 + x)
+    elif kind == "all sizes":
+        x = x * 2.0**torch.randint(-30, 30, x.shape, device="cuda", generator=g)
+    else:
+        x = torch.full((rows, cols), 0.7, device="cuda")
+    new = lambda t: torch.zeros(rows, cols, dtype=t, device="cuda")  # noqa: E731
+    n = z.LayerNorm(x=x.to(BF16), h=new(BF16), mean=torch.zeros(rows, device="cuda"), rstd=torch.zeros(rows, device="cuda"),
+                    ckpt_xn=z.new_act8(rows, cols, z.ACT8_E4M3), eps=1e-5)
+    z.zero_layer_norm(n)
+    if kind != "equal":
+        check_forward(n, kind)
+    else:  # the mean's bound is taken 1 / sqrt(eps) times
+        assert float(n.h.float().abs().max()) <= 84 * U * 0.71 * 317
+        assert_close(n.mean, n.x[:, 0].double(), torch.full((rows,), 84 * U, dtype=torch.float64))
+
+
+def test_saved_codes_are_those_of_64_bits():
+    """A code differs only where the value lies within its error of the middle
+    of two codes. That error is taken at 4 units of 2^-24, roundings of fp32 sums
+    being spread evenly; the middles of e4m3 lie 2^-4 of the value apart at the
+    least, so of evenly spread values at most 2 * 4 * 2^-24 / 2^-4 = 2^-17 have
+    another code; and as many again where the largest value of a block of 32 does
+    and moves their common unit."""
+    rows, cols = 2048, 4096
+    n = forward(rows, cols)[0]
+    got = torch.tensor(decode_act8(n.ckpt_xn)[0])
+    want = torch.tensor(round_act8(layer_norm_reference(n, n.x_out)["xn"][0].cpu().numpy(), z.ACT8_E4M3))
+    assert int((got != want).sum()) <= 2.0**-17 * rows * cols * 2
