@@ -933,16 +933,26 @@ __global__ __launch_bounds__(256) void ffn_copy_kernel(CopyArgs c)
 }
 
 // The operands whose rows do not lie on 16 bytes or end inside a unit, copied to
-// the workspace and so aligned; the parts of split tiles come behind them.
+// the workspace and so aligned; the parts of split tiles come behind them. The
+// two sums of dh are read at the same offsets: of its two gradients, and of its
+// two weights, both stay where they are, at one stride, or both are copied.
 hipError_t copy_operands(FfnKind kind, FfnArgs& a, size_t bytes, hipStream_t s)
 {
+    bool stays[4];
+    int64_t strides[4];
+    int count = 0;
+    each_operand(kind, a, a.outputs, [&](const uint16_t*& p, int64_t& ld, int64_t, int64_t cols) {
+        strides[count] = ld;
+        stays[count++] = cols % 8 == 0 && on_16(p, ld);
+    });
+    for (int i = 0; kind == kFfnInput && i < count; i += 2) stays[i] = stays[i + 1] = stays[i] && stays[i + 1] && strides[i] == strides[i + 1];
     CopyArgs c{};
-    int n = 0;
+    int n = 0, at = 0;
     int64_t most = 0;
     char* to = reinterpret_cast<char*>(a.part);
     a.part = reinterpret_cast<float*>(to + bytes);
     each_operand(kind, a, a.outputs, [&](const uint16_t*& p, int64_t& ld, int64_t rows, int64_t cols) {
-        if (cols % 8 == 0 && on_16(p, ld)) return;
+        if (stays[at++]) return;
         const int64_t units = (cols + 7) / 8;
         c.from[n] = Operand{p, ld, rows, cols};
         c.to[n] = reinterpret_cast<uint16_t*>(to);
