@@ -712,13 +712,16 @@ using Small = Tile<64, 128, 2, 2, 4, 3>;
 using Flat = Tile<32, 128, 1, 2, 4, 4>;
 using Slow = Tile<128, 128, 2, 2, 2, 2>;  // through registers: a step takes 0.95 us with the chip full, Mid's 0.52
 
-// Whether 32-bit offsets reach over the 256 rows of a tile, the same ones in
-// both segments, and what runs across the summed index has a whole unit.
+// Whether 32-bit offsets reach over the 256 rows of a tile.
+bool in_reach(int64_t ld) { return ld <= (int64_t{1} << 22); }
+
+// Whether they do for all operands, the same ones in both segments, and what
+// runs across the summed index has a whole unit.
 template <FfnKind KIND>
 bool plain(const FfnArgs& a)
 {
-    const auto reach = [](int64_t ld) { return ld <= (int64_t{1} << 22); };
-    const bool h = reach(a.ld_h), d = reach(a.ld_d[0]) && reach(a.ld_d[1]), w = reach(a.ld_w[0]) && reach(a.ld_w[1]);
+    const bool h = in_reach(a.ld_h), w = in_reach(a.ld_w[0]) && in_reach(a.ld_w[1]);
+    const bool d = in_reach(a.ld_d[0]) && ((KIND == kFfnWeight && a.outputs == 1) || in_reach(a.ld_d[1]));
     if (KIND == kFfnForward) return h && w;
     if (KIND == kFfnInput) return d && w && a.ld_d[0] == a.ld_d[1] && a.ld_w[0] == a.ld_w[1] && a.cols >= 8;
     return d && h && a.hidden >= 8 && a.cols >= 8;
@@ -906,7 +909,7 @@ CopyPlan plan_unaligned(FfnKind kind, int outputs, int64_t rows, int64_t cols, i
     none.hidden = hidden;
     each_operand(kind, none, outputs, [&](const uint16_t*, int64_t, int64_t r, int64_t c) {
         const int64_t units = (c + 7) / 8;
-        if (c > (int64_t{1} << 22) - 8 || r > (int64_t{1} << 30) / units) fits = false;  // offsets of a tile; units in 32 bits
+        if (!in_reach(8 * units) || r > (int64_t{1} << 30) / units) fits = false;  // the latter: units in 32 bits
         else bytes += (static_cast<size_t>(r * units) * 16 + 255) / 256 * 256;
     });
     if (!fits) return here;
@@ -932,10 +935,11 @@ __global__ __launch_bounds__(256) void ffn_copy_kernel(CopyArgs c)
     *(ZERO_G u32x4*)(c.to[blockIdx.y] + static_cast<int64_t>(at) * 8) = load_unit(o.p + row * o.ld, int64_t{unit} * 8, o.cols);
 }
 
-// The operands whose rows do not lie on 16 bytes or end inside a unit, copied to
-// the workspace and so aligned; the parts of split tiles come behind them. The
-// two sums of dh are read at the same offsets: of its two gradients, and of its
-// two weights, both stay where they are, at one stride, or both are copied.
+// The operands whose rows do not lie on 16 bytes, end inside a unit or lie too
+// far apart, copied to the workspace, where they do not; the parts of split
+// tiles come behind them. The two sums of dh are read at the same offsets: of its
+// two gradients, and of its two weights, both stay where they are, at one stride,
+// or both are copied.
 hipError_t copy_operands(FfnKind kind, FfnArgs& a, size_t bytes, hipStream_t s)
 {
     bool stays[4];
@@ -943,7 +947,7 @@ hipError_t copy_operands(FfnKind kind, FfnArgs& a, size_t bytes, hipStream_t s)
     int count = 0;
     each_operand(kind, a, a.outputs, [&](const uint16_t*& p, int64_t& ld, int64_t, int64_t cols) {
         strides[count] = ld;
-        stays[count++] = cols % 8 == 0 && on_16(p, ld);
+        stays[count++] = cols % 8 == 0 && on_16(p, ld) && in_reach(ld);
     });
     for (int i = 0; kind == kFfnInput && i < count; i += 2) stays[i] = stays[i + 1] = stays[i] && stays[i + 1] && strides[i] == strides[i + 1];
     CopyArgs c{};
@@ -970,8 +974,8 @@ hipError_t copy_operands(FfnKind kind, FfnArgs& a, size_t bytes, hipStream_t s)
 template <FfnKind KIND>
 hipError_t launch_kind(FfnArgs a, hipStream_t s)
 {
-    a.plain = plain<KIND>(a);
     a.outputs = KIND == kFfnWeight && a.out[1].p != nullptr ? 2 : 1;
+    a.plain = plain<KIND>(a);
     FfnPlan plan;
     if (fast<KIND>(a)) {
         plan = plan_for(KIND, true, a.outputs, a.rows, a.cols, a.hidden).plan;
@@ -981,6 +985,7 @@ hipError_t launch_kind(FfnArgs a, hipStream_t s)
         if (odd.bytes > 0) {
             const hipError_t e = copy_operands(KIND, a, odd.bytes, s);
             if (e != hipSuccess) return e;
+            if (!plain<KIND>(a)) return hipErrorInvalidValue;  // the tiles that are launched below go by it
         }
     }
     a.chunk = plan.chunk;

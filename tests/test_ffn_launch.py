@@ -86,7 +86,7 @@ def check(host, kind, outputs, rows, cols, hidden, operands):
 # columns that are a multiple of 8 or not, of one operand, both or none
 SIZES = [(300, 767, 520), (2011, 1003, 2736), (900, 1003, 1024), (2011, 1000, 2731), (2011, 1024, 2731), (8192, 4096, 11003), (640, 767, 1001),
          (300, 264, 520), (16, 1003, 2731), (5, 7, 9), (64, 4091, 11003), (700, 8, 11)]
-PLACES = [(0, 0), (0, 8), (0, 16), (0, 3), (2, 0), (2, 8)]  # address, columns more than there are
+PLACES = [(0, 0), (0, 8), (0, 16), (0, 3), (2, 0), (2, 8), (0, FAR), (0, 8 * FAR)]  # address, columns more than there are
 
 
 @pytest.mark.parametrize("kind,outputs", [(FORWARD, 1), (INPUT, 1), (WEIGHT, 1), (WEIGHT, 2)])

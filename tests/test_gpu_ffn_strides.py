@@ -51,3 +51,24 @@ def test_pairs_of_operands_that_lie_differently(rows, cols, hidden, pair, first,
         place.check()
     for k, w in zip(RESULTS, want):
         assert torch.equal(getattr(b, k), w), k
+
+
+def far_apart(t, ld):
+    """t in rows of `ld` elements."""
+    v = torch.empty((t.shape[0] - 1) * ld + t.shape[1], dtype=t.dtype, device="cuda").as_strided(t.shape, (ld, 1))
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("names,rows,cols,hidden,ld", [(("dgate", "dup"), 300, 767, 520, 1 << 22), (("dgate",), 300, 767, 520, 1 << 23),
+                                                       (("w_gate", "w_up"), 300, 520, 767, 1 << 22), (("h",), 300, 520, 767, 1 << 25)])
+def test_rows_that_32_bit_offsets_do_not_reach(names, rows, cols, hidden, ld):
+    r = backward(rows, cols, hidden, saved="raw", accumulate=False)
+    b = r[0]
+    want = [getattr(b, k).clone() for k in RESULTS]
+    for k in names:
+        setattr(b, k, far_apart(getattr(b, k), ld + 8))
+    again(b, (rows, cols, hidden))
+    check_backward(*r)
+    for k, w in zip(RESULTS, want):
+        assert torch.equal(getattr(b, k), w), k
