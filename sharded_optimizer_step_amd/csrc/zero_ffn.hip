@@ -149,7 +149,7 @@ template <int TO>
 __device__ __forceinline__ void load_to_lds(i32x4 buffer, uint32_t offset, uint32_t base)
 {
     asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 : : "s"(base), "v"(offset), "s"(buffer), "n"(TO) : "memory", "scc");
+                 : : "s"(base), "v"(offset), "s"(buffer), "n"(TO) : "memory", "scc", "m0");
 }
 
 // 8 summed elements for this lane's row or column of a piece of 16, from a tile
