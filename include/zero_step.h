@@ -832,9 +832,10 @@ int zero_block_norm_grad(const zero_block_norm_grad_args* args, void* ws, size_t
  * within 84 * 2^-24 * mean(|x_out|); each result is then rounded to its own type
  * once.
  *
- * Range. A row with an inf or NaN, or whose sum passes fp32's range, has NaN in
- * its mean, rstd, xn and h; one whose squares pass it has rstd 0. With eps 0 a
- * row of equal values has a large or infinite rstd, and anything in xn.
+ * Range. A row with an inf or NaN has NaN in its mean, rstd, xn and h, and so
+ * may one whose sum passes fp32's range; one whose squares pass it may have rstd
+ * 0. With eps 0 a row of equal values has a large or infinite rstd, and anything
+ * in xn.
  */
 typedef struct zero_layer_norm_args {
     int64_t rows;     /* 0 <= rows < 2^31 */
@@ -887,8 +888,9 @@ typedef struct zero_layer_norm_grad_args {
     int32_t flags;       /* ZERO_GRAD_ACCUMULATE: dw and db are fp32 and added to */
 } zero_layer_norm_grad_args;
 
-/* Workspace size of zero_layer_norm_grad (partial column sums); 0 on invalid
- * sizes. */
+/* Workspace size of zero_layer_norm_grad (partial column sums, and for rows of
+ * more than 8192 columns two values a row), the same whichever of dw and db are
+ * wanted; 0 on invalid sizes. */
 size_t zero_layer_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
 
 /* ws: as in zero_block_norm_grad. */
@@ -907,10 +909,14 @@ int zero_layer_norm_grad(const zero_layer_norm_grad_args* args, void* ws, size_t
 /*
  * zero_block_ffn -- both projections, the activation and the product in one
  * pass. gate and up are summed in fp32 in an order that depends only on the
- * sizes and on which operands' rows lie on 16 bytes, and a is made from these
- * sums. For the backward pass they can be kept
- * as bf16 rows (gate, up) or as act8 buffers (ckpt_gate, ckpt_up), or neither;
- * each result is rounded to its own type once. cols == 0: the sums are 0.
+ * sizes, on which operands' rows lie on 16 bytes and on whether one's lie more
+ * than 2^22 elements apart, and a is made from these sums: within
+ * (32 + 4 |gate|) 2^-24 |gate * up| of the formula of them. (Where act(gate) is
+ * far smaller than gate that is more than bf16's half step: of ZERO_FFN_GELU from
+ * gate = -5 down; at -8, where it is -5e-15, 1% of it.) For the backward pass the
+ * sums can be kept as bf16 rows (gate, up) or as act8 buffers (ckpt_gate,
+ * ckpt_up), or neither; each result is rounded to its own type once. cols == 0:
+ * the sums are 0.
  * rows < 2^31, cols and hidden <= 2^30, rows times either (rounded up to 32)
  * < 2^36, and fewer than 2^20 tiles of 128 x 128 of rows x hidden, rows x cols
  * and hidden x cols. Two outputs at one address are refused.
@@ -949,8 +955,10 @@ int zero_block_ffn(const zero_block_ffn_args* args, void* ws, size_t ws_bytes, h
  * dgate and dup are the nearest bf16 values of the formulas (computed in fp32,
  * and in fp64 where that leaves the rounding open); dh and the weight gradients
  * are those of dgate and dup as stored, summed in fp32 in an order that depends
- * only on the sizes, on which of them are wanted and on which operands' rows lie
- * on 16 bytes, each rounded to its own type once.
+ * only on the sizes, on which of them are wanted and on how the operands lie
+ * (which rows lie on 16 bytes, whether dgate and dup have one stride and w_gate
+ * and w_up one, whether a stride is over 2^22 elements), each rounded to its own
+ * type once.
  * The block's input comes as bf16 rows h, or as the act8 buffer ckpt_h whose
  * decoded columns are multiplied with col_scale (cols values, bf16 or fp32;
  * absent: ones), as in zero_act8_wgrad. ckpt_a, if given, is written: the act8

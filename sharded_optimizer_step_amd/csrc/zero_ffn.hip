@@ -10,11 +10,14 @@
 // transposing LDS reads turn it.
 //
 // Many rows are bound by the matrix instructions, and at 68 to 72% of their
-// cycles by the chip's power: 8192 rows x 4096 x 11008 (1.48 TFLOP each)
-// forward 1.22 ms (1.21 PFLOP/s), dh 1.07 ms (1.38), both weight gradients
-// 1.16 ms (1.27); a library's plain products of these sizes reach 1.24 to 1.57.
-// Few rows are bound by reading the weights: one row 40 us, 180 MB at 4.5 TB/s.
-// Small products are bound by latency: 192 x 768 x 2048 forward 9 us.
+// cycles by the chip's power. 8192 rows x 4096 x 11008 (1.48 TFLOP each), the
+// median of nine profiled launches and their least: forward 1.38 and 1.22 ms
+// (1.07 and 1.21 PFLOP/s; 1.17 to 1.21 ms a call in a row), dh 1.09 and 1.07 (1.35
+// and 1.38), both weight gradients 1.20 and 1.16 (1.23 and 1.27); a library's plain
+// products of these sizes reach 1.24 to 1.57. Few rows are bound by reading the
+// weights: one row 44 and 40 us, 180 MB at 4.1 and 4.5 TB/s (reads reach 7.0): 172
+// workgroups leave a third of the chip without one. Small products are bound by
+// latency: 192 x 768 x 2048 forward 9.3 and 9.2 us.
 #include <type_traits>
 #include <utility>
 

@@ -9,10 +9,11 @@
 // bound on its error, and where the bf16 value is not the same on both sides
 // of that, in fp64. One in about a thousand is.
 //
-// Bound by HBM and the fp32 form together: 8192 x 11008 from 8 bits 160 us, 727
-// MB at 4.5 TB/s (219 with one kernel for all activations and the two gradients'
-// roundings checked one after the other); the error function's form 27.6 us for
-// 2011 x 2731, where its instructions take most of the time.
+// Bound by HBM and the fp32 form together: 8192 x 11008 from 8 bits 168 us in the
+// median and 160 at the least, 727 MB at 4.3 and 4.5 TB/s (219 with one kernel for
+// all activations and the two gradients' roundings checked one after the other);
+// the error function's form 28.1 and 27.6 us for 2011 x 2731 (44 MB), where erfcf's
+// instructions take most of the time.
 #include "zero_act8_device.h"
 
 namespace zero {

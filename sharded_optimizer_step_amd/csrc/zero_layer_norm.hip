@@ -3,10 +3,14 @@
 //
 // A row stays in the registers of L lanes, V vectors of 8 columns a lane, so
 // every operand is read once and every result written once. Both passes are
-// streams, bound by HBM: 16384 x 4096 forward with x_out and 8 bits saved 113
-// us (606 MB, 5.4 TB/s), backward from 8 bits 92 us (472 MB, 5.1 TB/s) and 5 to
-// join the column sums; unaligned fp32 rows of 5003, backward, 56 us (240 MB, 4.3
-// TB/s). A short call is bound by its launch: 128 x 768 4.8 us.
+// streams, bound by HBM. Medians of nine launches and the least of them: 16384 x
+// 4096 forward with x_out and 8 bits saved 114 and 108 us (606 MB, 5.3 and 5.6
+// TB/s), backward from 8 bits 94 and 92 us (472 MB, 5.0 and 5.1 TB/s) and 5 to join
+// the column sums; unaligned fp32 rows of 5003, backward, 58 and 56 us (240 MB, 4.1
+// and 4.3 TB/s). Rows of more than 8192 columns have nothing in flight across a
+// row's sums forward, and are read twice backward: 6000 x 11008 bf16 154 us a call
+// (3.4 TB/s), backward 165 from 8 bits and 181 from rows (2.9). A short call is
+// bound by its launch: 128 x 768 5.0 and 4.8 us.
 #include "zero_norm_device.h"
 
 namespace zero {
@@ -89,7 +93,8 @@ __device__ __forceinline__ Moments moments(float (&x)[V][8], int lane, int lanes
     }
     r = wave_sum(r);
     q = wave_sum(q);
-    // Joined in fp64: D is a small sum of terms as large as the waves' means lie apart.
+    // Joined in fp64: D is a small sum of terms as large as the waves' means lie apart. (Each d itself is an fp32
+    // difference, off by 2^-24 of how far the two waves lie apart: no more than the squares about it bear.)
     float first = m;
     double step, squares;
     if constexpr (WAVE) {
